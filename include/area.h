@@ -454,6 +454,112 @@ int area_window_attn_noalloc(const void* q, const void* k, const void* v,
                              size_t plan_bytes, void* o, int H, int D,
                              float scale, int dtype, cudaStream_t stream);
 
+/* ---- attention over a key/value cache ---------------------------------- */
+
+/*
+ * The calls of this section serve models that generate token by token or
+ * chunk by chunk next to the calls above: a sampler that keeps the keys and
+ * values of what it has made so far.  The pages have no counterpart.
+ *
+ * Shared by all of them:
+ *   - k, v : [B, Hk, S, D] is a cache with room for S tokens per sequence, of
+ *     which the first lens[b] are valid.  lens is int32 [B] in device memory,
+ *     or null (every sequence has S tokens); a length outside 0 .. S is cut to
+ *     it.  Rows of the cache from lens[b] on are never used: they may hold
+ *     anything, NaN included.
+ *   - q, o : [B, H, Nq, D].  Query head h reads key head h / (H / Hk); Hk
+ *     divides H.  The Nq queries of a sequence are its last Nq tokens (their
+ *     keys and values are in the cache already): query i sits at position
+ *     p = lens[b] - Nq + i.  A query that sees no key (p < 0: a sequence
+ *     shorter than Nq, padded in front) gets a row of zeros.
+ *   - A non-finite key or value that some query of a sequence sees may reach
+ *     every output row of the calls' sequences that read that key head.
+ *   - ws   : workspace of ws_bytes >= area_*_ws_bytes() (host only, from the
+ *     sizes alone; 0 = none, ws may then be null), 32-byte aligned.  Contents
+ *     on entry are ignored, on exit unspecified; calls that may overlap on
+ *     the GPU need one each.
+ *   - Sums run in a fixed order: outputs are bit-identical from run to run
+ *     and in CUDA-graph replays.
+ *   - scale is positive.  dtype: bf16 or fp32; D: 64 or 128.
+ * Errors of all of them: AREA_EINVAL (null, bad size, misaligned buffer),
+ * AREA_EUNSUPPORTED (dtype, D, or sizes past 32-bit row
+ * indexes: B * H * Nq, P + S above 2^31 - 257), AREA_ENOSPACE, AREA_ECUDA.
+ */
+
+/*
+ * area_sink_attn -- causal attention over a sliding window and the first
+ * tokens, which stay visible:
+ *   o = softmax(scale * q K_V^T) V_V,
+ *   V = { j <= p : j > p - window or j < sinks }.
+ * Serves a whole prompt (Nq = S), a chunk of one, and single new tokens
+ * (Nq = 1); only the keys of V are read.  window >= S gives plain causal
+ * attention.
+ */
+int area_sink_attn_ws_bytes(int B, int H, int Hk, int Nq, int S, int D,
+                            int window, int sinks, int dtype,
+                            size_t* ws_bytes);
+int area_sink_attn(const void* q, const void* k, const void* v,
+                   const int* lens, void* o, void* ws, size_t ws_bytes,
+                   int B, int H, int Hk, int Nq, int S, int D, int window,
+                   int sinks, float scale, int dtype, cudaStream_t stream);
+
+/*
+ * area_prefix_attn -- attention of a batch whose sequences share a prefix:
+ * every query attends to the P shared keys kp, vp [Hk, P, D], held once for
+ * the whole batch, and to its own sequence's keys,
+ *   causal = 1: prefix and own keys j <= p; a query with p < 0 sees nothing
+ *   causal = 0: prefix and own keys j < lens[b], for every query (several
+ *               images of one prompt that share its text keys)
+ * P = 0 (kp, vp null) or S = 0 (k, v null; lens is then not read) leave that
+ * part out; one of them is positive.  When a sequence has few queries (fewer
+ * than 64 rows per key head) the prefix is read once for the batch, all
+ * sequences' rows against it, and joined with the own keys' part.
+ */
+int area_prefix_attn_ws_bytes(int B, int H, int Hk, int Nq, int P, int S,
+                              int D, int dtype, size_t* ws_bytes);
+int area_prefix_attn(const void* q, const void* kp, const void* vp,
+                     const void* k, const void* v, const int* lens, void* o,
+                     void* ws, size_t ws_bytes, int B, int H, int Hk, int Nq,
+                     int P, int S, int D, int causal, float scale, int dtype,
+                     cudaStream_t stream);
+
+/*
+ * area_cache_attn -- causal attention over the whole cache that also adds up
+ * how much weight each key has received, the measure that area_cache_evict
+ * goes by:
+ *   o    = softmax(scale * q K^T) V over j <= p
+ *   acco[b, hk, j] = acc[b, hk, j] + sum of the softmax weights of key j over
+ *          the H / Hk query heads of hk and the Nq queries
+ * acc, acco : fp32 [B, Hk, S]; acc null counts as zeros; acco may be acc.
+ * Entries from lens[b] on are copied.
+ */
+int area_cache_attn_ws_bytes(int B, int H, int Hk, int Nq, int S, int D,
+                             int dtype, size_t* ws_bytes);
+int area_cache_attn(const void* q, const void* k, const void* v,
+                    const int* lens, const float* acc, void* o, float* acco,
+                    void* ws, size_t ws_bytes, int B, int H, int Hk, int Nq,
+                    int S, int D, float scale, int dtype, cudaStream_t stream);
+
+/*
+ * area_cache_evict -- shrinks every sequence of a cache to at most `budget`
+ * tokens.  A sequence of n = lens[b] <= budget tokens keeps them all;
+ * otherwise each key head keeps its first `sinks` tokens, its last `recent`
+ * and, of those between, the budget - sinks - recent of largest acc (ties: the
+ * lowest index; a NaN counts as -infinity), in their order.
+ *   ko, vo : [B, Hk, So, D] kept rows; rows from lenso[b] on are left as they
+ *            were.  So >= budget.
+ *   acco   : fp32 [B, Hk, So] their weights, zeros from lenso[b] on
+ *   lenso  : int32 [B], min(n, budget);  idx : int32 [B, Hk, So] the kept
+ *            tokens' old positions, -1 from lenso[b] on
+ * In place: ko = k, vo = v and acco = acc, all three, with So = S.  Any other
+ * overlap of an output with an input or another output is refused.
+ */
+int area_cache_evict(const void* k, const void* v, const float* acc,
+                     const int* lens, void* ko, void* vo, float* acco,
+                     int* lenso, int* idx, int B, int Hk, int S, int So, int D,
+                     int budget, int sinks, int recent, int dtype,
+                     cudaStream_t stream);
+
 /*
  * area_test_plan_barrier_expiry -- TEST HOOK, not part of the method (the
  * pages have no counterpart).  Runs the one-launch detail map + planner of

@@ -37,7 +37,10 @@ EXPORTED = ("area_status_string", "area_last_cuda_error", "area_version", "area_
             "area_window_plan", "area_window_attn_ws_bytes", "area_window_attn_stage_bytes",
             "area_window_attn_bridge_stage_bytes",
             "area_window_attn",
-            "area_window_attn_noalloc", "area_test_plan_barrier_expiry")
+            "area_window_attn_noalloc", "area_test_plan_barrier_expiry",
+            "area_sink_attn_ws_bytes", "area_sink_attn", "area_prefix_attn_ws_bytes",
+            "area_prefix_attn", "area_cache_attn_ws_bytes", "area_cache_attn",
+            "area_cache_evict")
 
 
 class AreaError(RuntimeError):
@@ -91,6 +94,13 @@ _SIGS = {
     "area_bridge_lattice": (_I, [_I, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)]),
     "area_phase_switch": (_I, [_P, _I, _F, ctypes.POINTER(_I)]),
     "area_schedule": (_I, [_P, _I, _F, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "area_sink_attn_ws_bytes": (_I, [_I] * 9 + [ctypes.POINTER(_SZ)]),
+    "area_sink_attn": (_I, [_P] * 6 + [_SZ] + [_I] * 8 + [_F, _I, _P]),
+    "area_prefix_attn_ws_bytes": (_I, [_I] * 8 + [ctypes.POINTER(_SZ)]),
+    "area_prefix_attn": (_I, [_P] * 8 + [_SZ] + [_I] * 8 + [_F, _I, _P]),
+    "area_cache_attn_ws_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_SZ)]),
+    "area_cache_attn": (_I, [_P] * 8 + [_SZ] + [_I] * 6 + [_F, _I, _P]),
+    "area_cache_evict": (_I, [_P] * 9 + [_I] * 9 + [_P]),
     "area_bridge_select_ws_bytes": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "area_bridge_select": (_I, [_P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "area_window_attn_bridge": (_I, [_P, _P, _P, _P, _I, ctypes.POINTER(area_plan_cfg), _P, _SZ,
@@ -326,6 +336,57 @@ def area_window_attn_bridge(q, k, v, cand, R, cfg: area_plan_cfg, plan, plan_byt
                                           ctypes.byref(cfg), _ptr(plan), plan_bytes, _ptr(o),
                                           _ptr(ws), ws_bytes, H, D, scale, dtype,
                                           _stream(stream)), "area_window_attn_bridge")
+
+
+def area_sink_attn_ws_bytes(B: int, H: int, Hk: int, Nq: int, S: int, D: int, window: int,
+                            sinks: int, dtype: int) -> int:
+    out = _SZ(0)
+    _check(_lib().area_sink_attn_ws_bytes(B, H, Hk, Nq, S, D, window, sinks, dtype,
+                                          ctypes.byref(out)), "area_sink_attn_ws_bytes")
+    return out.value
+
+
+def area_sink_attn(q, k, v, lens, o, ws, ws_bytes, B, H, Hk, Nq, S, D, window, sinks, scale, dtype,
+                   stream=None) -> None:
+    _check(_lib().area_sink_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(o), _ptr(ws), ws_bytes,
+                                 B, H, Hk, Nq, S, D, window, sinks, scale, dtype,
+                                 _stream(stream)), "area_sink_attn")
+
+
+def area_prefix_attn_ws_bytes(B: int, H: int, Hk: int, Nq: int, P: int, S: int, D: int,
+                              dtype: int) -> int:
+    out = _SZ(0)
+    _check(_lib().area_prefix_attn_ws_bytes(B, H, Hk, Nq, P, S, D, dtype, ctypes.byref(out)),
+           "area_prefix_attn_ws_bytes")
+    return out.value
+
+
+def area_prefix_attn(q, kp, vp, k, v, lens, o, ws, ws_bytes, B, H, Hk, Nq, P, S, D, causal, scale,
+                     dtype, stream=None) -> None:
+    _check(_lib().area_prefix_attn(_ptr(q), _ptr(kp), _ptr(vp), _ptr(k), _ptr(v), _ptr(lens),
+                                   _ptr(o), _ptr(ws), ws_bytes, B, H, Hk, Nq, P, S, D, causal,
+                                   scale, dtype, _stream(stream)), "area_prefix_attn")
+
+
+def area_cache_attn_ws_bytes(B: int, H: int, Hk: int, Nq: int, S: int, D: int, dtype: int) -> int:
+    out = _SZ(0)
+    _check(_lib().area_cache_attn_ws_bytes(B, H, Hk, Nq, S, D, dtype, ctypes.byref(out)),
+           "area_cache_attn_ws_bytes")
+    return out.value
+
+
+def area_cache_attn(q, k, v, lens, acc, o, acco, ws, ws_bytes, B, H, Hk, Nq, S, D, scale, dtype,
+                    stream=None) -> None:
+    _check(_lib().area_cache_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(acc), _ptr(o),
+                                  _ptr(acco), _ptr(ws), ws_bytes, B, H, Hk, Nq, S, D, scale,
+                                  dtype, _stream(stream)), "area_cache_attn")
+
+
+def area_cache_evict(k, v, acc, lens, ko, vo, acco, lenso, idx, B, Hk, S, So, D, budget, sinks,
+                     recent, dtype, stream=None) -> None:
+    _check(_lib().area_cache_evict(_ptr(k), _ptr(v), _ptr(acc), _ptr(lens), _ptr(ko), _ptr(vo),
+                                   _ptr(acco), _ptr(lenso), _ptr(idx), B, Hk, S, So, D, budget,
+                                   sinks, recent, dtype, _stream(stream)), "area_cache_evict")
 
 
 def parse_plan(buf: np.ndarray) -> dict:

@@ -1,0 +1,226 @@
+// extern "C" entry points of the key/value cache: argument validation, the
+// launches of a call and the layout of its workspace.
+#include <limits.h>
+#include <math.h>
+
+#include "cache.cuh"
+
+namespace area {
+namespace {
+
+constexpr int64_t kSms = 148;        // B200; the workspace's size may not hang on the device
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t ceil256(int64_t n) { return (n + 255) & ~int64_t(255); }
+
+// Splits of `keys` keys for `blocks` row blocks: enough blocks for four on
+// each SM, at least two tiles of 64 keys to a split.
+int simt_splits(int64_t blocks, int64_t keys) {
+  const int64_t most = cdiv(keys, 128), want = cdiv(4 * kSms, blocks);
+  const int64_t n = want < most ? want : most;
+  return n < 1 ? 1 : (int)n;
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+}  // namespace
+
+int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int window, int sinks,
+               int dtype, CachePlan* p) {
+  if (dtype != AREA_DTYPE_F32 && dtype != AREA_DTYPE_BF16) return AREA_EUNSUPPORTED;
+  if (B < 1 || H < 1 || Hk < 1 || Nq < 1 || P < 0 || S < 0) return AREA_EINVAL;
+  if (H % Hk || window < 1 || sinks < 0) return AREA_EINVAL;
+  if (S < 1 && P < 1) return AREA_EINVAL;
+  if (D != 64 && D != 128) return AREA_EUNSUPPORTED;
+  // row and key indexes are 32-bit, a key list may hold prefix and cache
+  if ((int64_t)P + S > INT_MAX - 256) return AREA_EUNSUPPORTED;
+  if ((int64_t)B * H > INT_MAX) return AREA_EUNSUPPORTED;
+  p->rows = (int64_t)B * H * Nq;
+  if (p->rows > INT_MAX) return AREA_EUNSUPPORTED;
+  const int R = H / Hk * Nq;
+  const bool pool = op == CACHE_OP_PREFIX && P > 0 && B > 1 && R < 64;
+  p->pooled = CacheLaunch{};
+  CacheLaunch& m = p->main;
+  m = CacheLaunch{};
+  m.used = !pool || S > 0;
+  const bool per_head = Nq >= 64;
+  m.rows = CacheRows{per_head ? Nq : R, per_head ? B * H : B * Hk, per_head ? H / Hk : 1, 0,
+                     P > 0 && !pool, S > 0};
+  m.wide = m.rows.RG > 16;
+  const int64_t M = m.wide ? 64 : 16;
+  // keys that a row block can see at most
+  int64_t own = (int64_t)sinks + window + (per_head ? M : Nq);
+  if (own > S) own = S;
+  m.nsplit = simt_splits(m.rows.groups * cdiv(m.rows.RG, M), own + (m.rows.use_prefix ? P : 0));
+  p->slots = m.used ? m.nsplit : 0;
+  if (pool) {
+    CacheLaunch& l = p->pooled;
+    l.used = true;
+    l.rows = CacheRows{B * R, Hk, 1, R, 1, 0};
+    l.wide = B * R > 16;
+    l.nsplit = simt_splits(Hk * cdiv(l.rows.RG, l.wide ? 64 : 16), P);
+    p->slots += l.nsplit;
+  }
+  if (p->slots == 1 && op != CACHE_OP_WEIGHTS) p->slots = 0;
+  p->off_ml = 0;
+  p->off_o = p->off_ml + ceil256(p->slots * p->rows * 8);
+  p->off_lse = p->off_o + ceil256(p->slots * p->rows * D * 4);
+  p->off_logits = p->off_lse + (op == CACHE_OP_WEIGHTS ? ceil256(p->rows * 4) : 0);
+  p->bytes = p->off_logits + (op == CACHE_OP_WEIGHTS ? ceil256(p->rows * S * 4) : 0);
+  const int64_t blocks = (int64_t)m.rows.groups * cdiv(m.rows.RG, M) * m.nsplit;
+  if (blocks > INT_MAX || cdiv(S, 256) * B * Hk > INT_MAX) return AREA_EUNSUPPORTED;
+  return AREA_OK;
+}
+
+namespace {
+
+int finish(cudaError_t e) { return e == cudaSuccess ? AREA_OK : fail_cuda(e); }
+
+int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco, void* ws,
+               size_t ws_bytes, int dtype, cudaStream_t s) {
+  if (!a.q || !a.o) return AREA_EINVAL;
+  CachePlan p;
+  const int st = cache_plan(op, a.B, a.H, a.Hk, a.Nq, a.P, a.S, a.D, a.window, a.sinks, dtype, &p);
+  if (st != AREA_OK) return st;
+  if ((a.S > 0 && (!a.k || !a.v)) || (a.P > 0 && (!a.kp || !a.vp))) return AREA_EINVAL;
+  if (!(scale > 0.f) || !isfinite(scale)) return AREA_EINVAL;
+  if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.kp, 16) ||
+      !aligned(a.vp, 16) || !aligned(a.o, 32) || !aligned(a.lens, 4))
+    return AREA_EINVAL;
+  if (ws_bytes < (size_t)p.bytes) return AREA_ENOSPACE;
+  if ((p.bytes > 0 && !ws) || !aligned(ws, 32)) return AREA_EINVAL;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  char* w = static_cast<char*>(ws);
+  CacheOut out{};
+  out.direct = p.slots == 0;
+  out.rows = p.rows;
+  if (p.slots) {
+    out.part_ml = reinterpret_cast<float2*>(w + p.off_ml);
+    out.part_o = reinterpret_cast<float*>(w + p.off_o);
+  }
+  if (op == CACHE_OP_WEIGHTS) out.logits = reinterpret_cast<float*>(w + p.off_logits);
+  cudaError_t e;
+  const CacheLaunch* ls[2] = {&p.main, &p.pooled};
+  for (const CacheLaunch* l : ls) {
+    if (!l->used) continue;
+    out.nsplit = l->nsplit;
+    if ((e = launch_cache_simt(a, l->rows, out, dtype, l->wide, s)) != cudaSuccess)
+      return fail_cuda(e);
+    out.slot0 += l->nsplit;
+  }
+  if (!p.slots) return AREA_OK;
+  float* lse = op == CACHE_OP_WEIGHTS ? reinterpret_cast<float*>(w + p.off_lse) : nullptr;
+  e = launch_cache_join(a, out.part_o, out.part_ml, p.slots, p.rows, lse, dtype, s);
+  if (e != cudaSuccess || op != CACHE_OP_WEIGHTS) return finish(e);
+  return finish(launch_cache_weights(a, out.logits, lse, acc, acco, s));
+}
+
+int ws_bytes_of(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int window, int sinks,
+                int dtype, size_t* ws_bytes) {
+  if (!ws_bytes) return AREA_EINVAL;
+  CachePlan p;
+  const int st = cache_plan(op, B, H, Hk, Nq, P, S, D, window, sinks, dtype, &p);
+  if (st == AREA_OK) *ws_bytes = (size_t)p.bytes;
+  return st;
+}
+
+}  // namespace
+}  // namespace area
+
+extern "C" {
+
+int area_sink_attn_ws_bytes(int B, int H, int Hk, int Nq, int S, int D, int window, int sinks,
+                            int dtype, size_t* ws_bytes) {
+  if (S < 1) return AREA_EINVAL;
+  return area::ws_bytes_of(area::CACHE_OP_SINK, B, H, Hk, Nq, 0, S, D, window, sinks, dtype,
+                           ws_bytes);
+}
+
+int area_sink_attn(const void* q, const void* k, const void* v, const int* lens, void* o, void* ws,
+                   size_t ws_bytes, int B, int H, int Hk, int Nq, int S, int D, int window,
+                   int sinks, float scale, int dtype, cudaStream_t stream) {
+  if (S < 1) return AREA_EINVAL;
+  area::CacheArgs a{q, k, v, nullptr, nullptr, lens, o, B, H, Hk, Nq, 0, S, D, window, sinks, 1, 0.f};
+  return area::cache_call(area::CACHE_OP_SINK, a, scale, nullptr, nullptr, ws, ws_bytes, dtype,
+                          stream);
+}
+
+int area_prefix_attn_ws_bytes(int B, int H, int Hk, int Nq, int P, int S, int D, int dtype,
+                              size_t* ws_bytes) {
+  return area::ws_bytes_of(area::CACHE_OP_PREFIX, B, H, Hk, Nq, P, S, D, INT_MAX, 0, dtype,
+                           ws_bytes);
+}
+
+int area_prefix_attn(const void* q, const void* kp, const void* vp, const void* k, const void* v,
+                     const int* lens, void* o, void* ws, size_t ws_bytes, int B, int H, int Hk,
+                     int Nq, int P, int S, int D, int causal, float scale, int dtype,
+                     cudaStream_t stream) {
+  if (causal != 0 && causal != 1) return AREA_EINVAL;
+  area::CacheArgs a{q, k, v, kp, vp, lens, o, B, H, Hk, Nq, P, S, D, INT_MAX, 0, causal, 0.f};
+  return area::cache_call(area::CACHE_OP_PREFIX, a, scale, nullptr, nullptr, ws, ws_bytes, dtype,
+                          stream);
+}
+
+int area_cache_attn_ws_bytes(int B, int H, int Hk, int Nq, int S, int D, int dtype,
+                             size_t* ws_bytes) {
+  if (S < 1) return AREA_EINVAL;
+  return area::ws_bytes_of(area::CACHE_OP_WEIGHTS, B, H, Hk, Nq, 0, S, D, INT_MAX, 0, dtype,
+                           ws_bytes);
+}
+
+int area_cache_attn(const void* q, const void* k, const void* v, const int* lens, const float* acc,
+                    void* o, float* acco, void* ws, size_t ws_bytes, int B, int H, int Hk, int Nq,
+                    int S, int D, float scale, int dtype, cudaStream_t stream) {
+  if (S < 1 || !acco || !area::aligned(acco, 4) || !area::aligned(acc, 4)) return AREA_EINVAL;
+  area::CacheArgs a{q, k, v, nullptr, nullptr, lens, o, B, H, Hk, Nq, 0, S, D, INT_MAX, 0, 1, 0.f};
+  return area::cache_call(area::CACHE_OP_WEIGHTS, a, scale, acc, acco, ws, ws_bytes, dtype, stream);
+}
+
+int area_cache_evict(const void* k, const void* v, const float* acc, const int* lens, void* ko,
+                     void* vo, float* acco, int* lenso, int* idx, int B, int Hk, int S, int So,
+                     int D, int budget, int sinks, int recent, int dtype, cudaStream_t stream) {
+  using area::aligned;
+  using area::overlap;
+  if (!k || !v || !acc || !ko || !vo || !acco || !lenso || !idx) return AREA_EINVAL;
+  if (B < 1 || Hk < 1 || S < 1 || So < 1) return AREA_EINVAL;
+  if (budget < 1 || budget > So || sinks < 0 || recent < 0 ||
+      (int64_t)sinks + recent > budget)
+    return AREA_EINVAL;
+  if (dtype != AREA_DTYPE_F32 && dtype != AREA_DTYPE_BF16) return AREA_EUNSUPPORTED;
+  if (D != 64 && D != 128) return AREA_EUNSUPPORTED;
+  if (S > INT_MAX - 4096 || So > INT_MAX - 4096) return AREA_EUNSUPPORTED;   // 32-bit indexes
+  const int64_t heads = (int64_t)B * Hk, elem = dtype == AREA_DTYPE_F32 ? 4 : 2;
+  if (heads > INT_MAX || heads * (2 * D * elem / 64 + 1) > INT_MAX ||
+      heads * area::cdiv(budget, 64) > INT_MAX)
+    return AREA_EUNSUPPORTED;                                                // grid sizes
+  for (const void* p : {k, v, (const void*)ko, (const void*)vo})
+    if (!aligned(p, 16)) return AREA_EINVAL;
+  for (const void* p : {(const void*)acc, (const void*)lens, (const void*)acco,
+                        (const void*)lenso, (const void*)idx})
+    if (!aligned(p, 4)) return AREA_EINVAL;
+  // in place: all three of k, v and acc; otherwise no output may touch an input
+  const bool in_place = k == ko || v == vo || acc == acco;
+  if (in_place && (k != ko || v != vo || acc != acco || S != So)) return AREA_EINVAL;
+  const int64_t nin = heads * S, nout = heads * So;
+  struct Buf { const void* p; int64_t n; };
+  const Buf in[4] = {{k, nin * D * elem}, {v, nin * D * elem}, {acc, nin * 4}, {lens, lens ? B * 4ll : 0}};
+  const Buf to[5] = {{lenso, B * 4ll}, {idx, nout * 4}, {ko, nout * D * elem},
+                     {vo, nout * D * elem}, {acco, nout * 4}};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (!(in_place && i >= 2 && j == i - 2) && overlap(to[i].p, to[i].n, in[j].p, in[j].n))
+        return AREA_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return AREA_EINVAL;
+  }
+  const area::EvictArgs e{k, v, acc, lens, ko, vo, acco, lenso, idx, B, Hk, S, So, D,
+                          budget, sinks, recent, (int)elem};
+  return area::finish(area::launch_cache_evict(e, stream));
+}
+
+}  // extern "C"

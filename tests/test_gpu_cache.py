@@ -1,0 +1,511 @@
+"""Attention over a key/value cache and its eviction against the float64 oracle.
+
+Tolerance of an output (derived, per element).  With u the half step of the
+storage type (bf16 2^-8, fp32 2^-24) and A = sum_j w_j |v_j|:
+  * storing the output rounds it once: u |o|;
+  * bf16: the weights are rounded to bf16 once before they meet the values:
+    2^-8 A;
+  * a score is a sum of D products in fp32: off by at most
+    d = D 2^-24 scale sum_d |q_d k_d| (plus its scaling, d again); a weight
+    exp(s - m) by 2 d relative, a normalised weight by 4 d: 4 d A;
+  * exponentials and the final division: a few fp32 steps, 2^-20 A;
+  * the sum over n keys in fp32: rounding errors of either sign, eight
+    standard deviations of n of them: 8 sqrt(n) 2^-24 A.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import step_adaptive_sparse_b200 as area
+from oracle import cache_oracle as co
+
+pytestmark = pytest.mark.gpu
+
+INT_MAX = 2 ** 31 - 1
+NAN = float("nan")
+TYPES = {"bf16": (torch.bfloat16, area.AREA_DTYPE_BF16, 2.0 ** -8),
+         "f32": (torch.float32, area.AREA_DTYPE_F32, 2.0 ** -24)}
+PAD = 64             # guard values before and after every output
+
+
+class Guarded:
+    """A device tensor inside a larger buffer filled with a marker."""
+
+    def __init__(self, shape, dtype, fill=None):
+        n = int(np.prod(shape))
+        self.buf = torch.full((n + 2 * PAD,), 77.0 if dtype.is_floating_point else 77, dtype=dtype, device="cuda")
+        self.t = self.buf[PAD:PAD + n].view(*shape)
+        if fill is not None:
+            self.t.fill_(fill)
+
+    def check(self):
+        assert (self.buf[:PAD] == 77).all() and (self.buf[-PAD:] == 77).all(), "guard values overwritten"
+
+
+def make(seed, dtype, B, H, Hk, Nq, S, D, lens, P=0, poison=True):
+    """Inputs on the device and their exact values as float64 arrays; the rows
+    behind each sequence and the queries before its first token are NaN."""
+    g = torch.Generator().manual_seed(seed)
+    t = TYPES[dtype][0]
+    q = (torch.randn(B, H, Nq, D, generator=g) * 1.5).to(t)
+    k, v = torch.randn(B, Hk, S, D, generator=g).to(t), torch.randn(B, Hk, S, D, generator=g).to(t)
+    kp, vp = torch.randn(Hk, P, D, generator=g).to(t), torch.randn(Hk, P, D, generator=g).to(t)
+    if poison:
+        for b, n in enumerate(lens):
+            n = min(max(n, 0), S)
+            k[b, :, n:] = NAN
+            v[b, :, n:] = NAN
+    host = [x.double().numpy() for x in (q, k, v, kp, vp)]
+    dev = [x.cuda() for x in (q, k, v, kp, vp)]
+    return dev, host, torch.tensor(lens, dtype=torch.int32).cuda()
+
+
+def workspace(nb):
+    # filled with NaN: what a call does not write it may not read
+    w = Guarded((max(nb // 4, 8),), torch.float32, NAN)
+    return w
+
+
+def bound(host, o, size, dtype, scale, n):
+    q, k, _, kp, _ = host
+    u = TYPES[dtype][2]
+    kk = np.nan_to_num(np.abs(k))
+    G = q.shape[1] // k.shape[1]
+    top = np.maximum(kk.max(2, initial=0), np.abs(kp).max(1, initial=0)[None]).repeat(G, 1)   # [B, H, D]
+    D = q.shape[-1]
+    d = D * 2.0 ** -24 * scale * (np.abs(q) * top[:, :, None]).sum(-1, keepdims=True)
+    w = 2.0 ** -8 if dtype == "bf16" else 0.0
+    return u * np.abs(o) + (w + 4 * d + 2.0 ** -20 + 8 * math.sqrt(max(n, 1)) * 2.0 ** -24) * size + 1e-30
+
+
+def close(got, want, tol):
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    bad = np.abs(got - want) - tol
+    assert bad.max() <= 0, f"off by {np.abs(got - want).max():.3e}, {bad.max():.3e} over, at {np.unravel_index(bad.argmax(), bad.shape)}"
+
+
+def run_sink(dev, lens, dtype, window, sinks, scale, o, stream=None, ws=None):
+    q, k, v, _, _ = dev
+    B, H, Nq, D = q.shape
+    Hk, S = k.shape[1:3]
+    dt = TYPES[dtype][1]
+    nb = area.area_sink_attn_ws_bytes(B, H, Hk, Nq, S, D, window, sinks, dt)
+    w = ws or workspace(nb)
+    area.area_sink_attn(q, k, v, lens, o, w.t, nb, B, H, Hk, Nq, S, D, window, sinks, scale, dt, stream)
+    return w
+
+
+def run_prefix(dev, lens, dtype, causal, scale, o, stream=None, ws=None):
+    q, k, v, kp, vp = dev
+    B, H, Nq, D = q.shape
+    Hk, S, P = k.shape[1], k.shape[2], kp.shape[1]
+    dt = TYPES[dtype][1]
+    nb = area.area_prefix_attn_ws_bytes(B, H, Hk, Nq, P, S, D, dt)
+    w = ws or workspace(nb)
+    area.area_prefix_attn(q, kp if P else None, vp if P else None, k if S else None, v if S else None,
+                          lens, o, w.t, nb, B, H, Hk, Nq, P, S, D, causal, scale, dt, stream)
+    return w
+
+
+def run_cache(dev, lens, dtype, scale, acc, o, acco, stream=None, ws=None):
+    q, k, v, _, _ = dev
+    B, H, Nq, D = q.shape
+    Hk, S = k.shape[1:3]
+    dt = TYPES[dtype][1]
+    nb = area.area_cache_attn_ws_bytes(B, H, Hk, Nq, S, D, dt)
+    w = ws or workspace(nb)
+    area.area_cache_attn(q, k, v, lens, acc, o, acco, w.t, nb, B, H, Hk, Nq, S, D, scale, dt, stream)
+    return w
+
+
+# ---- sliding window with sinks ---------------------------------------------------------------
+
+SINK = [
+    # B, H, Hk, Nq, S, D, window, sinks, lens
+    (1, 1, 1, 1, 1, 64, 1, 0, [1]),
+    (1, 2, 1, 1, 5, 128, 1, 1, [5]),
+    (5, 4, 2, 1, 130, 64, 64, 4, [0, 1, 64, 65, 130]),
+    (4, 8, 2, 1, 1000, 128, 129, 4, [1000, 999, 127, 3]),
+    (2, 8, 8, 1, 700, 128, INT_MAX, 0, [700, 513]),
+    (3, 5, 5, 3, 333, 64, 50, 70, [333, 2, 71]),
+    (2, 16, 1, 1, 2049, 128, 700, 0, [2049, 1]),
+    (1, 16, 1, 2, 513, 64, 100, 7, [513]),
+    (2, 6, 2, 8, 200, 128, 33, 500, [200, 5]),
+    (1, 4, 1, 17, 300, 64, 16, 3, [300]),
+    (2, 12, 4, 40, 160, 128, 65, 1, [160, 39]),
+    (1, 2, 2, 64, 64, 128, 20, 2, [64]),
+    (2, 2, 1, 65, 65, 64, 64, 0, [65, 64]),
+    (1, 3, 3, 127, 400, 128, 128, 130, [400]),
+    (1, 2, 1, 128, 128, 64, 128, 0, [128]),
+    (2, 4, 2, 257, 257, 128, 100, 5, [257, 129]),
+    (1, 2, 2, 300, 900, 64, 256, 1, [850]),
+    (1, 2, 1, 513, 1024, 128, 384, 129, [1000]),
+    (2, 2, 2, 640, 640, 128, INT_MAX, 0, [640, 333]),
+    (1, 1, 1, 700, 700, 64, 1, 0, [700]),
+    (1, 2, 1, 520, 520, 128, 5, 400, [520]),
+    (1, 2, 2, 1100, 1100, 64, 900, 64, [1100]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S,D,window,sinks,lens", SINK)
+def test_sink_attention(B, H, Hk, Nq, S, D, window, sinks, lens, dtype):
+    dev, host, dl = make(1, dtype, B, H, Hk, Nq, S, D, lens)
+    scale = D ** -0.5
+    o = Guarded((B, H, Nq, D), TYPES[dtype][0], NAN)
+    w = run_sink(dev, dl, dtype, window, sinks, scale, o.t)
+    want, _, size = co.cache_attention(*host[:3], lens, scale, window=window, sinks=sinks)
+    close(o.t, want, bound(host, want, size, dtype, scale, S))
+    o.check(), w.check()
+    again = torch.full_like(o.t, NAN)
+    run_sink(dev, dl, dtype, window, sinks, scale, again)
+    assert torch.equal(again, o.t)
+    assert area.area_kernel_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lengths_outside_the_cache_are_cut_and_null_means_full(dtype):
+    B, H, Hk, Nq, S, D = 3, 4, 2, 2, 90, 64
+    dev, host, dl = make(2, dtype, B, H, Hk, Nq, S, D, [90, 90, 90])
+    a, b, c = (torch.full_like(dev[0], NAN) for _ in range(3))
+    run_sink(dev, dl, dtype, 40, 2, 0.125, a)
+    run_sink(dev, None, dtype, 40, 2, 0.125, b)
+    run_sink(dev, torch.tensor([91, 10 ** 9, INT_MAX], dtype=torch.int32).cuda(), dtype, 40, 2, 0.125, c)
+    assert torch.equal(a, b) and torch.equal(a, c)
+    run_sink(dev, torch.tensor([-1, 0, -INT_MAX - 1], dtype=torch.int32).cuda(), dtype, 40, 2, 0.125, c)
+    assert (c == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Nq", [1, 200])
+def test_keys_outside_every_window_may_hold_anything(Nq, dtype):
+    """Neither the tokens between the sinks and the first window nor scores of
+    the lowest or highest finite value disturb a row."""
+    B, H, Hk, S, D, window, sinks = 1, 4, 2, 600, 128, 70, 3
+    dev, host, dl = make(3, dtype, B, H, Hk, Nq, S, D, [S])
+    lo = S - Nq + 1 - window
+    a, b = (torch.full_like(dev[0], NAN) for _ in range(2))
+    run_sink(dev, dl, dtype, window, sinks, 0.1, a)
+    for x in dev[1:3]:
+        x[:, :, sinks:lo] = NAN
+    run_sink(dev, dl, dtype, window, sinks, 0.1, b)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Nq", [1, 140])
+def test_large_scores(Nq, dtype):
+    """Scores far apart, and growing along the keys, so that the running
+    maximum moves by much in every tile."""
+    B, H, Hk, S, D = 1, 2, 1, 700, 64
+    dev, host, dl = make(4, dtype, B, H, Hk, Nq, S, D, [S])
+    ramp = torch.linspace(-40, 40, S)[:, None].cuda()
+    dev[1].copy_((dev[1].float() * 0.05 + ramp * torch.sign(dev[0][0, 0, 0].float())).to(dev[1].dtype))
+    host[1] = dev[1].double().cpu().numpy()
+    o = torch.full_like(dev[0], NAN)
+    run_sink(dev, dl, dtype, 300, 5, 0.125, o)
+    want, _, size = co.cache_attention(*host[:3], [S], 0.125, window=300, sinks=5)
+    close(o, want, bound(host, want, size, dtype, 0.125, S))
+
+
+def test_window_of_everything_equals_full_attention():
+    """With one query row the new call and the library's full attention are the
+    same operation (the last row sees every key)."""
+    B, H, N, D = 1, 2, 384, 128
+    dev, host, dl = make(5, "bf16", B, H, H, N, N, D, [N])
+    o, full = torch.full_like(dev[0], NAN), torch.full_like(dev[0], NAN)
+    run_sink(dev, dl, "bf16", INT_MAX, 0, D ** -0.5, o)
+    area.area_full_attn(*dev[:3], full, B, H, N, D, D ** -0.5, area.AREA_DTYPE_BF16)
+    assert (o[:, :, -1].float() - full[:, :, -1].float()).abs().max() < 2e-2
+
+
+# ---- shared prefix ---------------------------------------------------------------------------
+
+PREFIX = [
+    # B, H, Hk, Nq, P, S, D, lens
+    (1, 1, 1, 1, 1, 1, 64, [1]),
+    (2, 2, 2, 1, 64, 1, 128, [1, 0]),
+    (4, 8, 8, 1, 700, 130, 64, [130, 64, 1, 65]),
+    (3, 8, 2, 1, 1000, 200, 128, [200, 3, 100]),
+    (17, 16, 1, 1, 333, 40, 64, [i % 41 for i in range(5, 22)]),
+    (2, 16, 2, 8, 129, 70, 128, [70, 5]),
+    (3, 5, 5, 3, 127, 30, 64, [30, 2, 17]),
+    (2, 6, 2, 21, 255, 64, 64, [64, 20]),
+    (2, 4, 2, 100, 300, 150, 128, [150, 99]),
+    (2, 2, 1, 300, 129, 300, 64, [300, 200]),
+    (1, 3, 3, 257, 64, 400, 128, [400]),
+    (5, 4, 2, 1, 500, 0, 128, [0, 0, 0, 0, 0]),
+    (3, 4, 2, 2, 0, 100, 64, [100, 1, 50]),
+    (1, 4, 2, 150, 200, 0, 64, [0]),
+    (40, 4, 4, 1, 2100, 33, 128, [33 - i % 34 for i in range(40)]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("B,H,Hk,Nq,P,S,D,lens", PREFIX)
+def test_prefix_attention(B, H, Hk, Nq, P, S, D, lens, causal, dtype):
+    dev, host, dl = make(6, dtype, B, H, Hk, Nq, S, D, lens, P=P)
+    scale = D ** -0.5
+    o = Guarded((B, H, Nq, D), TYPES[dtype][0], NAN)
+    w = run_prefix(dev, dl, dtype, causal, scale, o.t)
+    want, _, size = co.cache_attention(*host[:3], lens, scale, causal=bool(causal), kp=host[3], vp=host[4])
+    close(o.t, want, bound(host, want, size, dtype, scale, P + S))
+    o.check(), w.check()
+    again = torch.full_like(o.t, NAN)
+    run_prefix(dev, dl, dtype, causal, scale, again)
+    assert torch.equal(again, o.t)
+    assert area.area_kernel_error() == 0
+
+
+# ---- accumulated weights ---------------------------------------------------------------------
+
+CACHE = [
+    # B, H, Hk, Nq, S, D, lens
+    (1, 1, 1, 1, 1, 64, [1]),
+    (3, 8, 2, 1, 513, 64, [513, 1, 0]),
+    (2, 8, 8, 1, 300, 128, [300, 257]),
+    (2, 16, 1, 1, 2000, 128, [2000, 129]),
+    (2, 6, 2, 5, 777, 64, [777, 3]),
+    (1, 4, 2, 33, 400, 128, [400]),
+    (2, 4, 4, 130, 260, 64, [260, 129]),
+    (1, 20, 1, 1, 150, 128, [140]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S,D,lens", CACHE)
+def test_cache_attention_and_weights(B, H, Hk, Nq, S, D, lens, dtype):
+    dev, host, dl = make(7, dtype, B, H, Hk, Nq, S, D, lens)
+    scale = D ** -0.5
+    o = Guarded((B, H, Nq, D), TYPES[dtype][0], NAN)
+    acco = Guarded((B, Hk, S), torch.float32, NAN)
+    acc = torch.rand(B, Hk, S, generator=torch.Generator().manual_seed(8)).cuda()
+    w = run_cache(dev, dl, dtype, scale, acc, o.t, acco.t)
+    want, got, size = co.cache_attention(*host[:3], lens, scale)
+    close(o.t, want, bound(host, want, size, dtype, scale, S))
+    o.check(), w.check(), acco.check()
+    # a weight is off by 4 d + 2^-20 relative (see above; d is at most this), the sums by one step per addition
+    q, k = host[0], np.nan_to_num(host[1])
+    d = D * 2.0 ** -24 * scale * np.abs(q).max() * np.abs(k).max() * D
+    rows = H // Hk * Nq
+    sums = acc.double().cpu().numpy() + got
+    close(acco.t, sums, got * (4 * d + 2.0 ** -20) + (rows + 2) * 2.0 ** -24 * sums)
+    # null counts as zeros, and the sums may be updated in place
+    zero, inplace = torch.full_like(acc, NAN), acc.clone()
+    run_cache(dev, dl, dtype, scale, None, o.t, zero)
+    run_cache(dev, dl, dtype, scale, inplace, o.t, inplace)
+    close(zero, got, got * (4 * d + 2.0 ** -20 + (rows + 2) * 2.0 ** -24))
+    assert torch.equal(inplace, acco.t)
+    assert area.area_kernel_error() == 0
+
+
+# ---- eviction --------------------------------------------------------------------------------
+
+EVICT = [
+    # B, Hk, S, So, D, budget, sinks, recent, lens, weights
+    (1, 1, 1, 1, 64, 1, 0, 0, [1], "plain"),
+    (2, 2, 600, 250, 64, 250, 4, 64, [600, 251], "plain"),
+    (3, 1, 1500, 1500, 128, 700, 0, 0, [1500, 700, 701], "plain"),
+    (2, 3, 1025, 64, 128, 33, 1, 32, [1025, 0], "plain"),
+    (1, 2, 3000, 2000, 64, 1999, 64, 1000, [2999], "ties"),
+    (1, 2, 3000, 100, 64, 99, 0, 10, [3000], "all equal"),
+    (1, 2, 2500, 600, 128, 600, 3, 7, [2500], "odd"),
+    (1, 1, 40, 40, 64, 10, 10, 0, [40], "plain"),
+    (1, 1, 40, 40, 64, 10, 0, 10, [40], "plain"),
+    (1, 1, 5000, 6000, 64, 4000, 5, 1, [5000], "ties"),
+    (2, 2, 20000, 9000, 64, 8999, 4, 500, [20000, 15001], "ties"),
+    (1, 1, 70001, 3001, 64, 3000, 4, 500, [70001], "plain"),
+]
+
+
+def weights_of(kind, shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    u = torch.rand(shape, generator=g)
+    if kind == "ties":
+        return torch.floor(u * 50) / 8
+    if kind == "all equal":
+        return torch.full(shape, 0.25)
+    if kind == "odd":
+        u[..., ::7], u[..., 1::9], u[..., 2::11] = NAN, float("inf"), -float("inf")
+        u[..., 3::5], u[..., 4::5] = 0.0, -0.0
+        u[..., 6::13] = -u[..., 6::13]
+        u[..., 10::17] = 1e-42
+    return u
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hk,S,So,D,budget,sinks,recent,lens,kind", EVICT)
+def test_eviction(B, Hk, S, So, D, budget, sinks, recent, lens, kind, dtype, in_place):
+    if in_place:
+        So = S = max(S, budget)
+    t = TYPES[dtype][0]
+    g = torch.Generator().manual_seed(11)
+    k, v = (Guarded((B, Hk, S, D), t) for _ in range(2))
+    acc = Guarded((B, Hk, S), torch.float32)
+    k.t.copy_(torch.randn(B, Hk, S, D, generator=g)), v.t.copy_(torch.randn(B, Hk, S, D, generator=g))
+    acc.t.copy_(weights_of(kind, (B, Hk, S), 12))
+    k0, v0, a0 = (x.t.cpu().clone() for x in (k, v, acc))
+    ko, vo = (k, v) if in_place else (Guarded((B, Hk, So, D), t, 5.0) for _ in range(2))
+    acco = acc if in_place else Guarded((B, Hk, So), torch.float32, NAN)
+    lenso, idx = Guarded((B,), torch.int32, -7), Guarded((B, Hk, So), torch.int32, -7)
+    dl = torch.tensor(lens, dtype=torch.int32).cuda()
+    area.area_cache_evict(k.t, v.t, acc.t, dl, ko.t, vo.t, acco.t, lenso.t, idx.t, B, Hk, S, So, D,
+                          budget, sinks, recent, TYPES[dtype][1])
+    torch.cuda.synchronize()
+    for x in (k, v, acc, ko, vo, acco, lenso, idx):
+        x.check()
+    assert lenso.t.tolist() == [min(n, budget) for n in lens]
+    gi, gk, gv, ga = (x.t.cpu() for x in (idx, ko, vo, acco))
+    for b, n in enumerate(lens):
+        for h in range(Hk):
+            keep = co.kept_tokens(a0[b, h].tolist(), n, budget, sinks, recent)
+            m = len(keep)
+            assert gi[b, h, :m].tolist() == keep and (gi[b, h, m:] == -1).all()
+            same = lambda x, y: torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))  # noqa: E731
+            assert same(gk[b, h, :m], k0[b, h, keep]) and same(gv[b, h, :m], v0[b, h, keep])
+            assert same(ga[b, h, :m], a0[b, h, keep]) and (ga[b, h, m:] == 0).all()
+            if in_place:
+                assert same(gk[b, h, m:], k0[b, h, m:]) and same(gv[b, h, m:], v0[b, h, m:])
+            else:
+                assert (gk[b, h, m:] == 5).all() and (gv[b, h, m:] == 5).all()
+
+
+def test_eviction_without_lengths():
+    B, Hk, S, D = 2, 2, 300, 64
+    k = torch.randn(B, Hk, S, D, device="cuda")
+    acc = torch.rand(B, Hk, S, device="cuda")
+    out = []
+    for lens in (None, torch.full((B,), S, dtype=torch.int32, device="cuda"),
+                 torch.full((B,), INT_MAX, dtype=torch.int32, device="cuda")):
+        ko, vo = torch.zeros(B, Hk, 100, D, device="cuda"), torch.zeros(B, Hk, 100, D, device="cuda")
+        acco, idx = torch.zeros(B, Hk, 100, device="cuda"), torch.zeros(B, Hk, 100, dtype=torch.int32, device="cuda")
+        lenso = torch.zeros(B, dtype=torch.int32, device="cuda")
+        area.area_cache_evict(k, k.clone(), acc, lens, ko, vo, acco, lenso, idx, B, Hk, S, 100, D, 100, 4, 20,
+                              area.AREA_DTYPE_F32)
+        out.append((ko, acco, idx, lenso))
+    for o in out[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(out[0], o))
+
+
+# ---- together, on streams and in graphs -------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_cache_is_filled_read_and_evicted(dtype):
+    """A prompt, then single tokens whose weights add up, an eviction in place
+    when the cache is full, more tokens: every output and every choice against
+    the oracle run beside it."""
+    B, H, Hk, S, D, prompt, budget = 2, 8, 2, 160, 64, 140, 90
+    t, dt, _ = TYPES[dtype]
+    scale = D ** -0.5
+    g = torch.Generator().manual_seed(21)
+    lens = [prompt, prompt - 30]
+    dev, host, dl = make(22, dtype, B, H, Hk, prompt, S, D, lens)
+    o = torch.full_like(dev[0], NAN)
+    run_sink(dev, dl, dtype, INT_MAX, 0, scale, o)
+    want, _, size = co.cache_attention(*host[:3], lens, scale)
+    close(o, want, bound(host, want, size, dtype, scale, S))
+    k, v, hk, hv = dev[1], dev[2], host[1], host[2]
+    acc, hacc = torch.zeros(B, Hk, S, device="cuda"), np.zeros((B, Hk, S))
+    lenso, idx = torch.zeros_like(dl), torch.zeros(B, Hk, S, dtype=torch.int32, device="cuda")
+    for step in range(40):
+        q1 = (torch.randn(B, H, 1, D, generator=g) * 1.5).to(t)
+        for x, hx in ((k, hk), (v, hv)):
+            new = torch.randn(B, Hk, D, generator=g).to(t)
+            for b in range(B):
+                x[b, :, lens[b]] = new[b].cuda()
+                hx[b, :, lens[b]] = new[b].double().numpy()
+        lens = [n + 1 for n in lens]
+        dl.copy_(torch.tensor(lens, dtype=torch.int32))
+        o1 = torch.full((B, H, 1, D), NAN, dtype=t, device="cuda")
+        run_cache((q1.cuda(), k, v, None, None), dl, dtype, scale, acc, o1, acc)
+        h1 = [q1.double().numpy(), hk, hv, host[3], host[4]]
+        want, got, size = co.cache_attention(*h1[:3], lens, scale)
+        close(o1, want, bound(h1, want, size, dtype, scale, S))
+        hacc += got
+        assert np.abs(acc.cpu().numpy() - hacc).max() < 1e-4
+        if max(lens) == S:
+            have = acc.cpu().numpy()
+            area.area_cache_evict(k, v, acc, dl, k, v, acc, lenso, idx, B, Hk, S, S, D, budget, 4, 30, dt)
+            for b in range(B):
+                for h in range(Hk):
+                    keep = co.kept_tokens(have[b, h], lens[b], budget, 4, 30)
+                    m = len(keep)
+                    assert idx[b, h, :m].tolist() == keep
+                    hk[b, h, :m], hv[b, h, :m] = hk[b, h, keep].copy(), hv[b, h, keep].copy()
+                    hacc[b, h, :m], hacc[b, h, m:] = hacc[b, h, keep].copy(), 0
+            lens = [min(n, budget) for n in lens]
+            assert lenso.tolist() == lens
+
+
+def test_replayed_graphs_and_other_streams_give_the_same():
+    """A prompt's and a token's calls captured together: replays follow the
+    inputs and the lengths that lie in the buffers, two graphs with workspaces
+    of their own run at once."""
+    B, H, Hk, S, D, P = 3, 8, 2, 900, 128, 400
+    cases = []
+    for seed in (31, 32):
+        dev, host, dl = make(seed, "bf16", B, H, Hk, 1, S, D, [900, 450, 70], P=P, poison=False)
+        cases.append((dev, dl))
+    acc = [torch.rand(B, Hk, S, device="cuda") for _ in cases]
+    outs = [[torch.full_like(c[0][0], NAN) for _ in range(3)] + [torch.full_like(a, NAN)]
+            for c, a in zip(cases, acc)]
+    wss = [[workspace(1 << 24) for _ in range(3)] for _ in cases]
+
+    def step(c, a, o, w, s):
+        run_sink(c[0], c[1], "bf16", 200, 4, 0.1, o[0], s, w[0])
+        run_prefix(c[0], c[1], "bf16", 1, 0.1, o[1], s, w[1])
+        run_cache(c[0], c[1], "bf16", 0.1, a, o[2], o[3], s, w[2])
+
+    eager = []
+    for lens in ([900, 450, 70], [64, 0, 129]):
+        for c, a, o, w in zip(cases, acc, outs, wss):
+            c[1].copy_(torch.tensor(lens, dtype=torch.int32))
+            step(c, a, o, w, None)
+        torch.cuda.synchronize()
+        eager.append([[x.clone() for x in o] for o in outs])
+    graphs, streams = [], [torch.cuda.Stream() for _ in cases]
+    for c, a, o, w, s in zip(cases, acc, outs, wss, streams):
+        g = torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=s):
+            step(c, a, o, w, torch.cuda.current_stream())
+        graphs.append(g)
+    for lens, want in zip(([900, 450, 70], [64, 0, 129]), eager):
+        torch.cuda.synchronize()
+        for c, o in zip(cases, outs):
+            c[1].copy_(torch.tensor(lens, dtype=torch.int32))
+            for x in o:
+                x.fill_(NAN)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+                g.replay()
+        torch.cuda.synchronize()
+        for o, e in zip(outs, want):
+            assert all(torch.equal(x, y) for x, y in zip(o, e))
+
+
+def test_long_cache_offsets_past_32_bits():
+    """A cache of more than 2^32 bytes and 2^31 values per tensor: the last
+    sequence's rows lie past both."""
+    B, H, Hk, S, D = 3, 2, 2, 2_900_000, 128
+    k = torch.zeros(B, Hk, S, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    assert k.numel() > 2 ** 31
+    n, tail = S - 5, 300
+    g = torch.Generator().manual_seed(41)
+    q = torch.randn(B, H, 1, D, generator=g).bfloat16()
+    kt, vt = (torch.randn(B, Hk, tail, D, generator=g).bfloat16() for _ in range(2))
+    k[:, :, n - tail:n], v[:, :, n - tail:n] = kt.cuda(), vt.cuda()
+    lens = torch.full((B,), n, dtype=torch.int32).cuda()
+    o = torch.full((B, H, 1, D), NAN, dtype=torch.bfloat16, device="cuda")
+    run_sink((q.cuda(), k, v, None, None), lens, "bf16", tail, 0, 0.1, o)
+    host = [x.double().numpy() for x in (q, kt, vt)] + [np.zeros((Hk, 0, D))] * 2
+    want, _, size = co.cache_attention(*host[:3], [tail] * B, 0.1)
+    close(o, want, bound(host, want, size, "bf16", 0.1, tail))
