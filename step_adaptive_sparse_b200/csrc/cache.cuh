@@ -141,10 +141,12 @@ __device__ __forceinline__ KeyList key_list(const CacheArgs& a, const CacheRows&
 // ---- host side ------------------------------------------------------------
 enum { CACHE_OP_SINK, CACHE_OP_PREFIX, CACHE_OP_WEIGHTS };
 
-// A launch of a call: the kernel (wide: 64 rows to a block, else 16), the rows
-// and the splits of their keys.
+// The kernels: CUDA cores with 16 or 64 rows to a block, the one for few rows.
+enum { CACHE_SIMT16, CACHE_SIMT64, CACHE_DEC };
+// A launch of a call: the kernel, the rows and the splits of their keys.
 struct CacheLaunch {
-  bool used, wide;
+  bool used;
+  int kernel;
   CacheRows rows;
   int nsplit;
 };
@@ -161,6 +163,8 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
 
 cudaError_t launch_cache_simt(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
                               int dtype, bool wide, cudaStream_t s);
+cudaError_t launch_cache_dec(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
+                             cudaStream_t s);
 // Joins `slots` partial results per row into o, and their log2-sum-exp into
 // lse when that is given.
 cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const float2* part_ml,

@@ -3,6 +3,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "cache.cuh"
 
 namespace area {
@@ -13,12 +15,27 @@ constexpr int64_t kSms = 148;        // B200; the workspace's size may not hang 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t ceil256(int64_t n) { return (n + 255) & ~int64_t(255); }
 
-// Splits of `keys` keys for `blocks` row blocks: enough blocks for four on
-// each SM, at least two tiles of 64 keys to a split.
-int simt_splits(int64_t blocks, int64_t keys) {
-  const int64_t most = cdiv(keys, 128), want = cdiv(4 * kSms, blocks);
-  const int64_t n = want < most ? want : most;
-  return n < 1 ? 1 : (int)n;
+int rows_per_block(int kernel, int RG) {
+  return kernel == CACHE_SIMT64 ? 64 : kernel == CACHE_DEC && RG <= 8 ? 8 : 16;
+}
+
+// Chooses a launch's kernel, and splits its keys (at most `keys` of them).
+void cut(CacheLaunch& l, int dtype, int64_t keys) {
+  const int RG = l.rows.RG;
+  l.used = true;
+  l.kernel = dtype == AREA_DTYPE_BF16 && RG <= 16 ? CACHE_DEC : RG <= 16 ? CACHE_SIMT16 : CACHE_SIMT64;
+  const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, RG));
+  int64_t n;
+  if (l.kernel == CACHE_DEC) {
+    // eight rounds of four blocks on each SM, so that the last round is a small
+    // share, with 512 keys to a split; where that leaves SMs idle, 128
+    n = std::min(cdiv(32 * kSms, blocks), cdiv(keys, 512));
+    if (blocks * n < 2 * kSms) n = std::min(cdiv(2 * kSms, blocks), cdiv(keys, 128));
+  } else {
+    // four blocks on each SM, at least two tiles of 64 keys to a split
+    n = std::min(cdiv(4 * kSms, blocks), cdiv(keys, 128));
+  }
+  l.nsplit = (int)std::max<int64_t>(n, 1);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -47,24 +64,18 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   p->pooled = CacheLaunch{};
   CacheLaunch& m = p->main;
   m = CacheLaunch{};
-  m.used = !pool || S > 0;
   const bool per_head = Nq >= 64;
   m.rows = CacheRows{per_head ? Nq : R, per_head ? B * H : B * Hk, per_head ? H / Hk : 1, 0,
                      P > 0 && !pool, S > 0};
-  m.wide = m.rows.RG > 16;
-  const int64_t M = m.wide ? 64 : 16;
-  // keys that a row block can see at most
-  int64_t own = (int64_t)sinks + window + (per_head ? M : Nq);
+  // keys that a block of 64 rows can see at most
+  int64_t own = (int64_t)sinks + window + (per_head ? 64 : Nq);
   if (own > S) own = S;
-  m.nsplit = simt_splits(m.rows.groups * cdiv(m.rows.RG, M), own + (m.rows.use_prefix ? P : 0));
+  if (!pool || S > 0) cut(m, dtype, own + (m.rows.use_prefix ? P : 0));
   p->slots = m.used ? m.nsplit : 0;
   if (pool) {
-    CacheLaunch& l = p->pooled;
-    l.used = true;
-    l.rows = CacheRows{B * R, Hk, 1, R, 1, 0};
-    l.wide = B * R > 16;
-    l.nsplit = simt_splits(Hk * cdiv(l.rows.RG, l.wide ? 64 : 16), P);
-    p->slots += l.nsplit;
+    p->pooled.rows = CacheRows{B * R, Hk, 1, R, 1, 0};
+    cut(p->pooled, dtype, P);
+    p->slots += p->pooled.nsplit;
   }
   if (p->slots == 1 && op != CACHE_OP_WEIGHTS) p->slots = 0;
   p->off_ml = 0;
@@ -72,7 +83,7 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   p->off_lse = p->off_o + ceil256(p->slots * p->rows * D * 4);
   p->off_logits = p->off_lse + (op == CACHE_OP_WEIGHTS ? ceil256(p->rows * 4) : 0);
   p->bytes = p->off_logits + (op == CACHE_OP_WEIGHTS ? ceil256(p->rows * S * 4) : 0);
-  const int64_t blocks = (int64_t)m.rows.groups * cdiv(m.rows.RG, M) * m.nsplit;
+  const int64_t blocks = cdiv(m.rows.RG, 8) * m.rows.groups * std::max(m.nsplit, 1);
   if (blocks > INT_MAX || cdiv(S, 256) * B * Hk > INT_MAX) return AREA_EUNSUPPORTED;
   return AREA_OK;
 }
@@ -109,8 +120,10 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
   for (const CacheLaunch* l : ls) {
     if (!l->used) continue;
     out.nsplit = l->nsplit;
-    if ((e = launch_cache_simt(a, l->rows, out, dtype, l->wide, s)) != cudaSuccess)
-      return fail_cuda(e);
+    e = l->kernel == CACHE_DEC
+            ? launch_cache_dec(a, l->rows, out, s)
+            : launch_cache_simt(a, l->rows, out, dtype, l->kernel == CACHE_SIMT64, s);
+    if (e != cudaSuccess) return fail_cuda(e);
     out.slot0 += l->nsplit;
   }
   if (!p.slots) return AREA_OK;

@@ -1,0 +1,330 @@
+// Attention over a key/value cache for few query rows (bf16): one pass over
+// the keys, which is what bounds it.
+//
+// A block has up to 8 NT rows of a group and four warps, which take the keys
+// 16 at a time in turn.  The products are taken transposed, so that 8 rows
+// fill a whole mma.m16n8k16 and no row is padded beyond that:
+//   S^T (16 keys x 8 rows)    = K (16 x D)    Q^T (D x 8)
+//   O^T (D x 8 rows)          = V^T (D x 16)  P^T (16 x 8)
+// Keys and values go from global memory into the fragments without passing
+// through shared memory: a fragment's order of the summed index is free as
+// long as both operands agree, so a thread takes 16 contiguous bytes of a key
+// row as the fragments of two k-steps, and 16 bytes of each of four value rows,
+// interleaved pairwise, as those of four 16 x 16 blocks of V^T.  Each buffer
+// is loaded again as soon as the products have read it, so that a warp keeps
+// 16 keys and values (8 KB at D = 128) in flight.
+// The softmax keeps one reference per row and rescales only when a score
+// exceeds it by more than 2^8 (numerator and denominator use the same one, so
+// the result is exact); the weights are rounded once, to bf16, for the second
+// product.  mma.sync is enough here: at 8 rows the products take a fifth of
+// the time that the keys take to arrive.
+#include "cache.cuh"
+
+namespace area {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kStep = 16;                    // keys of a warp and step
+constexpr int kTile = kWarps * kStep;        // keys of a block and step
+constexpr float kSlack = 8.f;                // log2 units
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Keys and values are read once: they need no place in L1.
+__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, (D == 64 ? 5 : 4) - NT)
+cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int nrb) {
+  constexpr int kRows = 8 * NT;
+  constexpr int kU = D / 32;                 // 16-byte loads of a thread per key row
+  constexpr int kG = D / 64;                 // 16-byte loads of a thread per value row
+  __shared__ int64_t s_row[kRows];
+  __shared__ KeySpan s_span[kRows];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ __align__(16) float s_o[kWarps][kRows][D];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = lane >> 2, c = lane & 3;
+  const int sp = blockIdx.x % out.nsplit;
+  const int rb = blockIdx.x / out.nsplit % nrb;
+  const int g = blockIdx.x / out.nsplit / nrb;
+  const int r0 = rb * kRows, r1 = min(r0 + kRows, rm.RG);
+  const int kvh = rm.pool_rows ? 0 : g / rm.kv_div;           // (b, key head)
+  const KeyList kl = key_list(a, rm, rm.pool_rows ? 0 : kvh / a.Hk, r0, r1);
+  const auto* kb = static_cast<const __nv_bfloat16*>(a.k) + (int64_t)kvh * a.S * D;
+  const auto* vb = static_cast<const __nv_bfloat16*>(a.v) + (int64_t)kvh * a.S * D;
+  const int64_t pbase = (int64_t)(rm.pool_rows ? g : kvh % a.Hk) * a.P * D;
+  const auto* kpb = static_cast<const __nv_bfloat16*>(a.kp) + pbase;
+  const auto* vpb = static_cast<const __nv_bfloat16*>(a.vp) + pbase;
+
+  if (tid < kRows) {
+    KeySpan s{0, 0};
+    int64_t row = -1;
+    if (r0 + tid < r1) {
+      const CacheRow cr = cache_row(a, rm, g, r0 + tid);
+      row = cr.row;
+      s = key_span(a, cache_len(a, cr.b), cr.i);
+    }
+    s_row[tid] = row;
+    s_span[tid] = s;
+  }
+  __syncthreads();
+
+  // this split's tiles of kTile keys
+  const int ntile = (kl.total + kTile - 1) / kTile;
+  const int t0 = (int)((int64_t)ntile * sp / out.nsplit);
+  const int t1 = (int)((int64_t)ntile * (sp + 1) / out.nsplit);
+
+  // the base address of key u of the list (past its end: the last key's)
+  auto key_at = [&](int u, const __nv_bfloat16* own, const __nv_bfloat16* pre) {
+    u = min(u, kl.total - 1);
+    if (u < kl.np) return pre + (int64_t)u * D;
+    const int w = u - kl.np;
+    return own + (int64_t)(w < kl.ns ? w : kl.lo + (w - kl.ns)) * D;
+  };
+  uint4 kf[2][kU], vf[4][kG];
+  auto load_k = [&](int u0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const __nv_bfloat16* p = key_at(u0 + n + 8 * h, kb, kpb) + 8 * c;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) kf[h][u] = load16(p + 32 * u);
+    }
+  };
+  auto load_v = [&](int u0) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int u = u0 + 2 * c + (h & 1) + 8 * (h >> 1);
+      const __nv_bfloat16* p = key_at(u, vb, vpb) + 8 * n;
+#pragma unroll
+      for (int q = 0; q < kG; ++q) {
+        vf[h][q] = load16(p + 64 * q);
+        // past the list: zeros, so that a weight of zero meets no other value
+        if (u >= kl.total) vf[h][q] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  int u0 = t0 * kTile + warp * kStep;
+  const int uend = min(t1 * kTile, kl.total);
+  if (u0 < uend) {
+    load_k(u0);
+    load_v(u0);
+  }
+
+  // queries: row n of each 8 rows, in the order of the key fragments
+  uint32_t qf[NT][kU][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t row = s_row[8 * t + n];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (row >= 0)
+        x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * D +
+                                            32 * u + 8 * c);
+      qf[t][u][0] = x.x, qf[t][u][1] = x.y, qf[t][u][2] = x.z, qf[t][u][3] = x.w;
+    }
+  }
+  // a thread's scores are those of rows 2c and 2c + 1 of each 8
+  KeySpan span[NT][2];
+  bool pre[NT][2], all = true;        // all: every row of the block sees the whole list
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = 8 * t + 2 * c + x;
+      span[t][x] = s_span[r];
+      pre[t][x] = s_row[r] >= 0 && sees_prefix(a, span[t][x]);
+      if (s_row[r] >= 0)
+        all = all && (kl.np == 0 || pre[t][x]) &&
+              (kl.total == kl.np ||
+               (span[t][x].hi - kl.lo == kl.total - kl.np - kl.ns && span[t][x].lo == kl.lo));
+    }
+  all = __all_sync(0xffffffffu, all);
+
+  float o[NT][kG * 4][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int i = 0; i < kG * 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
+    m[t][0] = m[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.f;
+  }
+
+  for (; u0 < uend; u0 += kTile) {
+    float s[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        mma_bf16(s[t], kf[0][u].x, kf[1][u].x, kf[0][u].y, kf[1][u].y, qf[t][u][0], qf[t][u][1]);
+        mma_bf16(s[t], kf[0][u].z, kf[1][u].z, kf[0][u].w, kf[1][u].w, qf[t][u][2], qf[t][u][3]);
+      }
+    }
+    if (u0 + kTile < uend) load_k(u0 + kTile);
+    // s[t][0..3]: key n of rows 2c, 2c + 1, then key n + 8
+    const bool whole = all && u0 + kStep <= uend;
+    bool grow = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        s[t][x] *= a.scale_log2;
+        if (!whole || out.logits) {
+          const int u = u0 + n + 8 * (x >> 1), w = u - kl.np;
+          const int key = w < kl.ns ? w : kl.lo + (w - kl.ns);
+          const bool in = u < uend && (u < kl.np ? pre[t][x & 1] : sees_own(a, span[t][x & 1], key));
+          if (out.logits && in) {
+            const int64_t row = s_row[8 * t + 2 * c + (x & 1)];
+            if (row >= 0) out.logits[row * a.S + key] = s[t][x];
+          }
+          if (!in) s[t][x] = -INFINITY;
+        }
+        grow = grow || s[t][x] > m[t][x & 1] + kSlack;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mx = fmaxf(s[t][x], s[t][x + 2]);
+#pragma unroll
+          for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+          const float mn = fmaxf(m[t][x], mx);
+          const float alpha = ex2(m[t][x] - (mn == -INFINITY ? 0.f : mn));
+          m[t][x] = mn;
+          l[t][x] *= alpha;
+#pragma unroll
+          for (int i = 0; i < kG * 4; ++i) {
+            o[t][i][x] *= alpha;
+            o[t][i][x + 2] *= alpha;
+          }
+        }
+    }
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        // nothing seen so far: every weight is 0
+        const float ref = m[t][x & 1] == -INFINITY ? 0.f : m[t][x & 1];
+        s[t][x] = ex2(s[t][x] - ref);
+        l[t][x & 1] += s[t][x];
+      }
+      pf[t][0] = transpose8x8(pack2(s[t][0], s[t][1]));
+      pf[t][1] = transpose8x8(pack2(s[t][2], s[t][3]));
+    }
+#pragma unroll
+    for (int q = 0; q < kG; ++q) {
+      const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&vf[0][q]);
+      const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&vf[1][q]);
+      const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&vf[2][q]);
+      const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&vf[3][q]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t a0 = __byte_perm(w0[w], w1[w], 0x5410), a1 = __byte_perm(w0[w], w1[w], 0x7632);
+        const uint32_t a2 = __byte_perm(w2[w], w3[w], 0x5410), a3 = __byte_perm(w2[w], w3[w], 0x7632);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_bf16(o[t][q * 4 + w], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+      }
+    }
+    if (u0 + kTile < uend) load_v(u0 + kTile);
+  }
+
+  // the warps' results: rows 2c, 2c + 1 and dims 64 q + 8 n + 2 w, + 1
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = 8 * t + 2 * c + x;
+#pragma unroll
+      for (int y = 4; y < 32; y <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], y);
+      if (n == 0) {
+        s_m[warp][r] = m[t][x];
+        s_l[warp][r] = l[t][x];
+      }
+#pragma unroll
+      for (int i = 0; i < kG * 4; ++i)
+        *reinterpret_cast<float2*>(&s_o[warp][r][64 * (i >> 2) + 8 * n + 2 * (i & 3)]) =
+            make_float2(o[t][i][x], o[t][i][x + 2]);
+    }
+  __syncthreads();
+  constexpr int kPer = 4;                    // columns of a thread
+  for (int e = tid; e < kRows * (D / kPer); e += kWarps * 32) {
+    const int r = e / (D / kPer), d = e % (D / kPer) * kPer;
+    const int64_t row = s_row[r];
+    if (row < 0) continue;
+    float mm = s_m[0][r];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, f[kPer] = {};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float al = ex2(s_m[w][r] - ref);
+      ll = fmaf(al, s_l[w][r], ll);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) f[i] = fmaf(al, s_o[w][r][d + i], f[i]);
+    }
+    if (out.direct) {
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) f[i] = ll == 0.f ? 0.f : f[i] * inv;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * D + d) =
+          make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+    } else {
+      const int64_t at = (int64_t)(out.slot0 + sp) * out.rows + row;
+      if (d == 0) out.part_ml[at] = make_float2(mm, ll);
+      if (ll != 0.f)
+        *reinterpret_cast<float4*>(out.part_o + at * D + d) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch(const CacheArgs& a, const CacheRows& rm, const CacheOut& out, cudaStream_t s) {
+  const int nrb = (rm.RG + 8 * NT - 1) / (8 * NT);
+  const int64_t grid = (int64_t)rm.groups * nrb * out.nsplit;
+  cache_dec_kernel<D, NT><<<(unsigned)grid, kWarps * 32, 0, s>>>(a, rm, out, nrb);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_dec(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
+                             cudaStream_t s) {
+  if (rm.RG <= 8) return a.D == 64 ? launch<64, 1>(a, rm, out, s) : launch<128, 1>(a, rm, out, s);
+  return a.D == 64 ? launch<64, 2>(a, rm, out, s) : launch<128, 2>(a, rm, out, s);
+}
+
+}  // namespace area
