@@ -3,7 +3,7 @@
 // include/area.h for the contract of each call.
 #include <stdio.h>
 
-#include "area_internal.cuh"
+#include "cache.cuh"
 
 namespace {
 thread_local int g_last_cuda_error = 0;
@@ -110,6 +110,10 @@ int area_kernel_error(int* code) {
   if (st != AREA_OK) return st;
   st = finish(area::read_and_clear_plan_error(&pl));
   if (st != AREA_OK) return st;
+  int ca = 0;
+  st = finish(area::read_and_clear_cache_tc_error(&ca));
+  if (st != AREA_OK) return st;
+  tc |= ca;
   *code = tc | (pl ? AREA_KERR_PLAN_BARRIER : 0);
   return AREA_OK;
 }

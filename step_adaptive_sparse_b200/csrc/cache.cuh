@@ -12,6 +12,10 @@
 // them up.
 #pragma once
 
+#include <limits.h>
+
+#include <algorithm>
+
 #include "area_internal.cuh"
 
 namespace area {
@@ -53,13 +57,9 @@ struct CacheOut {
 };
 
 __host__ __device__ __forceinline__ int cache_len(const CacheArgs& a, int b) {
-#ifdef __CUDA_ARCH__
   if (!a.lens) return a.S;
   const int n = a.lens[b];
   return n < 0 ? 0 : n > a.S ? a.S : n;      // a length outside the cache is cut to it
-#else
-  return a.S;
-#endif
 }
 
 // Own keys that query i of a sequence of len tokens sees: [lo, hi) and, below
@@ -68,17 +68,17 @@ __host__ __device__ __forceinline__ int cache_len(const CacheArgs& a, int b) {
 struct KeySpan {
   int lo, hi;
 };
-__device__ __forceinline__ KeySpan key_span(const CacheArgs& a, int len, int i) {
+__host__ __device__ __forceinline__ KeySpan key_span(const CacheArgs& a, int len, int i) {
   KeySpan s;
   s.hi = a.causal ? len - a.Nq + 1 + i : len;
   if (s.hi < 0) s.hi = 0;
   s.lo = s.hi > a.window ? s.hi - a.window : 0;
   return s;
 }
-__device__ __forceinline__ bool sees_prefix(const CacheArgs& a, KeySpan s) {
+__host__ __device__ __forceinline__ bool sees_prefix(const CacheArgs& a, KeySpan s) {
   return !a.causal || s.hi > 0;
 }
-__device__ __forceinline__ bool sees_own(const CacheArgs& a, KeySpan s, int j) {
+__host__ __device__ __forceinline__ bool sees_own(const CacheArgs& a, KeySpan s, int j) {
   return j < s.hi && (j >= s.lo || j < a.sinks);
 }
 
@@ -88,7 +88,7 @@ struct CacheRow {
   int64_t row;
   int b, i;
 };
-__device__ __forceinline__ CacheRow cache_row(const CacheArgs& a, const CacheRows& rm, int g,
+__host__ __device__ __forceinline__ CacheRow cache_row(const CacheArgs& a, const CacheRows& rm, int g,
                                               int r) {
   CacheRow c;
   if (rm.pool_rows) {
@@ -104,6 +104,18 @@ __device__ __forceinline__ CacheRow cache_row(const CacheArgs& a, const CacheRow
   return c;
 }
 
+// The indexes of the queries of rows [r0, r1) run over [i0, i1], or over all
+// where the rows pass from one head to the next.
+__host__ __device__ __forceinline__ void query_range(const CacheArgs& a, int r0, int r1, int& i0,
+                                                     int& i1) {
+  i0 = r0 % a.Nq;
+  i1 = (r1 - 1) % a.Nq;
+  if (r1 - r0 >= a.Nq || i1 < i0) {
+    i0 = 0;
+    i1 = a.Nq - 1;
+  }
+}
+
 // The keys that rows [r0, r1) of a group see between them, as one list: the
 // prefix, the sinks below the windows, the windows' union.
 struct KeyList {
@@ -112,20 +124,15 @@ struct KeyList {
   int lo;       // first key of the windows' union
   int total;    // keys in all
 };
-__device__ __forceinline__ KeyList key_list(const CacheArgs& a, const CacheRows& rm, int b, int r0,
-                                            int r1) {
+__host__ __device__ __forceinline__ KeyList key_list(const CacheArgs& a, const CacheRows& rm, int b,
+                                                     int r0, int r1) {
   KeyList l;
   l.np = rm.use_prefix ? a.P : 0;
   l.ns = l.lo = 0;
   l.total = l.np;
   if (rm.pool_rows || !rm.use_own) return l;
-  // the queries' indexes in [r0, r1) run over [i0, i1], or over all where the
-  // rows pass from one head to the next
-  int i0 = r0 % a.Nq, i1 = (r1 - 1) % a.Nq;
-  if (r1 - r0 >= a.Nq || i1 < i0) {
-    i0 = 0;
-    i1 = a.Nq - 1;
-  }
+  int i0, i1;
+  query_range(a, r0, r1, i0, i1);
   const int len = cache_len(a, b);
   const KeySpan first = key_span(a, len, i0), last = key_span(a, len, i1);
   if (!sees_prefix(a, last)) {       // every row before the first token
@@ -141,8 +148,9 @@ __device__ __forceinline__ KeyList key_list(const CacheArgs& a, const CacheRows&
 // ---- host side ------------------------------------------------------------
 enum { CACHE_OP_SINK, CACHE_OP_PREFIX, CACHE_OP_WEIGHTS };
 
-// The kernels: CUDA cores with 16 or 64 rows to a block, the one for few rows.
-enum { CACHE_SIMT16, CACHE_SIMT64, CACHE_DEC };
+// The kernels: CUDA cores with 16 or 64 rows to a block, the one for few rows,
+// the tensor-core one.
+enum { CACHE_SIMT16, CACHE_SIMT64, CACHE_DEC, CACHE_TC };
 // A launch of a call: the kernel, the rows and the splits of their keys.
 struct CacheLaunch {
   bool used;
@@ -173,6 +181,15 @@ cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const flo
 // 2^(logits[row][j] - lse[row]).
 cudaError_t launch_cache_weights(const CacheArgs& a, const float* logits, const float* lse,
                                  const float* acc, float* acco, cudaStream_t s);
+
+// Rows of a row tile of the tensor-core kernel: 128, or in a pooled launch as
+// many whole sequences' rows as fit.
+inline int tc_tile_rows(const CacheRows& rm) {
+  return rm.pool_rows ? 128 / rm.pool_rows * rm.pool_rows : 128;
+}
+cudaError_t launch_cache_tc(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
+                            cudaStream_t s);
+cudaError_t read_and_clear_cache_tc_error(int* code);
 
 struct EvictArgs {
   const void *k, *v;

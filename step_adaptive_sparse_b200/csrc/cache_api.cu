@@ -1,9 +1,6 @@
 // extern "C" entry points of the key/value cache: argument validation, the
 // launches of a call and the layout of its workspace.
-#include <limits.h>
 #include <math.h>
-
-#include <algorithm>
 
 #include "cache.cuh"
 
@@ -15,18 +12,47 @@ constexpr int64_t kSms = 148;        // B200; the workspace's size may not hang 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t ceil256(int64_t n) { return (n + 255) & ~int64_t(255); }
 
-int rows_per_block(int kernel, int RG) {
-  return kernel == CACHE_SIMT64 ? 64 : kernel == CACHE_DEC && RG <= 8 ? 8 : 16;
+// Rows that one work item of a kernel takes.
+int rows_per_block(int kernel, const CacheRows& rm) {
+  switch (kernel) {
+    case CACHE_TC: return 2 * tc_tile_rows(rm);
+    case CACHE_SIMT64: return 64;
+    case CACHE_DEC: return rm.RG <= 8 ? 8 : 16;
+    default: return 16;
+  }
+}
+
+// Splits of the tensor-core kernel's units: those that end first by a model of
+// its time.  A key tile takes a unit 1.8 us, starting and ending one 4 us, and
+// splits cost the join (5 us, and their outputs written and read again).
+int tc_splits(int64_t units, int64_t keys, int64_t rows, int D) {
+  const int64_t tiles = cdiv(keys, 128);
+  int best = 1;
+  double least = 0;
+  for (int n = 1; n <= 64 && n <= cdiv(tiles, 2); ++n) {
+    const double t = cdiv(units * n, kSms) * (4.0 + 1.8 * (double)cdiv(tiles, n)) +
+                     (n > 1 ? 5.0 + (double)rows * n * D * 8 / 5.0e6 : 0.0);
+    if (n == 1 || t < least) {
+      least = t;
+      best = n;
+    }
+  }
+  return best;
 }
 
 // Chooses a launch's kernel, and splits its keys (at most `keys` of them).
-void cut(CacheLaunch& l, int dtype, int64_t keys) {
+void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D) {
   const int RG = l.rows.RG;
   l.used = true;
-  l.kernel = dtype == AREA_DTYPE_BF16 && RG <= 16 ? CACHE_DEC : RG <= 16 ? CACHE_SIMT16 : CACHE_SIMT64;
-  const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, RG));
+  if (dtype == AREA_DTYPE_BF16)
+    l.kernel = RG <= 16 || op == CACHE_OP_WEIGHTS ? CACHE_DEC : CACHE_TC;
+  else
+    l.kernel = RG <= 16 ? CACHE_SIMT16 : CACHE_SIMT64;
+  const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, l.rows));
   int64_t n;
-  if (l.kernel == CACHE_DEC) {
+  if (l.kernel == CACHE_TC) {
+    n = tc_splits(blocks, keys, rows, D);
+  } else if (l.kernel == CACHE_DEC) {
     // eight rounds of four blocks on each SM, so that the last round is a small
     // share, with 512 keys to a split; where that leaves SMs idle, 128
     n = std::min(cdiv(32 * kSms, blocks), cdiv(keys, 512));
@@ -64,17 +90,18 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   p->pooled = CacheLaunch{};
   CacheLaunch& m = p->main;
   m = CacheLaunch{};
-  const bool per_head = Nq >= 64;
+  // one head's rows alone fill row tiles: heads need not share a tile
+  const bool per_head = Nq >= (dtype == AREA_DTYPE_BF16 ? 128 : 64);
   m.rows = CacheRows{per_head ? Nq : R, per_head ? B * H : B * Hk, per_head ? H / Hk : 1, 0,
                      P > 0 && !pool, S > 0};
-  // keys that a block of 64 rows can see at most
-  int64_t own = (int64_t)sinks + window + (per_head ? 64 : Nq);
+  // keys that a block of up to 256 rows can see at most
+  int64_t own = (int64_t)sinks + window + (per_head ? 256 : Nq);
   if (own > S) own = S;
-  if (!pool || S > 0) cut(m, dtype, own + (m.rows.use_prefix ? P : 0));
+  if (!pool || S > 0) cut(m, op, dtype, own + (m.rows.use_prefix ? P : 0), p->rows, D);
   p->slots = m.used ? m.nsplit : 0;
   if (pool) {
     p->pooled.rows = CacheRows{B * R, Hk, 1, R, 1, 0};
-    cut(p->pooled, dtype, P);
+    cut(p->pooled, op, dtype, P, p->rows, D);
     p->slots += p->pooled.nsplit;
   }
   if (p->slots == 1 && op != CACHE_OP_WEIGHTS) p->slots = 0;
@@ -122,6 +149,8 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     out.nsplit = l->nsplit;
     e = l->kernel == CACHE_DEC
             ? launch_cache_dec(a, l->rows, out, s)
+        : l->kernel == CACHE_TC
+            ? launch_cache_tc(a, l->rows, out, s)
             : launch_cache_simt(a, l->rows, out, dtype, l->kernel == CACHE_SIMT64, s);
     if (e != cudaSuccess) return fail_cuda(e);
     out.slot0 += l->nsplit;

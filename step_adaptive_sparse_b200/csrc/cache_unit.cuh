@@ -1,0 +1,132 @@
+// How the tensor-core kernel of cache_tc.cu cuts a launch into work units: two
+// row tiles of a group and a split of the list of keys that they see.  Integer
+// arithmetic alone, also compiled for the host and checked there.
+#pragma once
+
+#include "cache.cuh"
+
+namespace area {
+
+struct Unit {
+  int valid;
+  int g, sp;               // row group, split
+  int kvh, ph;             // (sequence, key head) of the own keys, key head of the prefix
+  int r0[2];               // first row of each row tile (RG: the tile has none)
+  int t0, nt;              // this split's first list tile and its tiles
+  int tp, ts;              // list tiles of the prefix, of the sinks
+  KeyList kl;
+  int hi;                  // end of the own keys in the list
+  int safe_lo, safe_hi;    // own rows that some query of the sequence sees, or zero fill
+  // tiles [0, lead) and [oa, ob) of this split are the row tile's
+  int lead[2], oa[2], ob[2];
+};
+static_assert(sizeof(Unit) <= 160, "unit record");
+
+struct UnitParams {
+  CacheArgs a;
+  CacheRows rm;
+  CacheOut out;
+  int nrb;                 // pairs of row tiles of a group
+  int tile_rows;           // rows of a row tile: 128, pooled: whole sequences
+  int units;
+  int heavy_first;         // row tiles from the last to the first, over all groups
+};
+
+// A key tile of a unit.
+struct Tile {
+  int kind;                // 0 prefix, 1 own
+  int j0, n;               // first key, keys
+  bool copy;               // copied row by row
+};
+__host__ __device__ __forceinline__ Tile tile_of(const Unit& u, int j) {
+  Tile t;
+  int i = u.t0 + j;
+  if (i < u.tp) {
+    t.kind = 0;
+    t.j0 = i * 128;
+    t.n = min(128, u.kl.np - t.j0);
+    t.copy = false;                        // its map ends with the prefix
+    return t;
+  }
+  i -= u.tp;
+  t.kind = 1;
+  if (i < u.ts) {
+    t.j0 = i * 128;
+    t.n = min(128, u.kl.ns - t.j0);
+  } else {
+    t.j0 = u.kl.lo + (i - u.ts) * 128;
+    t.n = min(128, u.hi - t.j0);
+  }
+  t.copy = t.n < 128 && !(t.j0 >= u.safe_lo && t.j0 + 128 <= u.safe_hi);
+  return t;
+}
+__host__ __device__ __forceinline__ bool is_active(const Unit& u, int t, int j) {
+  return j < u.lead[t] || (j >= u.oa[t] && j < u.ob[t]);
+}
+// First and last tile of a row tile; last < 0: it has none.
+__host__ __device__ __forceinline__ int first_tile(const Unit& u, int t) { return u.lead[t] > 0 ? 0 : u.oa[t]; }
+__host__ __device__ __forceinline__ int last_tile(const Unit& u, int t) {
+  return u.ob[t] > u.oa[t] ? u.ob[t] - 1 : u.lead[t] - 1;
+}
+
+// Unit idx of a launch; false behind the last one.
+__host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& u) {
+  const CacheArgs& a = p.a;
+  const CacheRows& rm = p.rm;
+  if (idx >= p.units) return false;
+  u.sp = idx % p.out.nsplit;
+  const int rest = idx / p.out.nsplit;
+  int rb;
+  if (p.heavy_first) {
+    u.g = rest % rm.groups;
+    rb = p.nrb - 1 - rest / rm.groups;
+  } else {
+    rb = rest % p.nrb;
+    u.g = rest / p.nrb;
+  }
+  u.r0[0] = rb * 2 * p.tile_rows;
+  u.r0[1] = min(u.r0[0] + p.tile_rows, rm.RG);
+  const int r1 = min(u.r0[0] + 2 * p.tile_rows, rm.RG);
+  u.kvh = rm.pool_rows ? 0 : u.g / rm.kv_div;
+  u.ph = rm.pool_rows ? u.g : u.kvh % a.Hk;
+  const int b = rm.pool_rows ? 0 : u.kvh / a.Hk;
+  u.kl = key_list(a, rm, b, u.r0[0], r1);
+  u.hi = u.kl.lo + (u.kl.total - u.kl.np - u.kl.ns);
+  u.tp = (u.kl.np + 127) / 128;
+  u.ts = (u.kl.ns + 127) / 128;
+  const int to = (u.hi - u.kl.lo + 127) / 128;
+  const int ntile = u.tp + u.ts + to;
+  u.t0 = (int)((int64_t)ntile * u.sp / p.out.nsplit);
+  const int t1 = (int)((int64_t)ntile * (u.sp + 1) / p.out.nsplit);
+  u.nt = t1 - u.t0;
+  u.safe_lo = u.safe_hi = 0;
+  if (!rm.pool_rows && rm.use_own) {
+    const int len = cache_len(a, b);
+    const int lo = key_span(a, len, 0).lo;
+    u.safe_lo = a.sinks >= lo ? 0 : lo;
+    u.safe_hi = len == a.S ? INT_MAX : len;      // the map fills with zeros from S on
+  }
+  for (int t = 0; t < 2; ++t) {
+    u.lead[t] = u.oa[t] = u.ob[t] = 0;
+    const int ra = u.r0[t], rz = t == 0 ? u.r0[1] : r1;
+    if (ra >= rz) continue;                      // no rows
+    u.lead[t] = max(0, min(u.nt, u.tp + u.ts - u.t0));
+    if (to == 0) continue;
+    int i0, i1;
+    query_range(a, ra, rz, i0, i1);
+    const int len = cache_len(a, b);
+    int lo = key_span(a, len, i0).lo;
+    const int hi = key_span(a, len, i1).hi;
+    if (hi <= lo) {                              // padding rows alone: nothing to see
+      u.lead[t] = 0;
+      continue;
+    }
+    if (a.sinks > u.kl.lo) lo = u.kl.lo;         // sinks among the first own tiles
+    const int base = u.tp + u.ts - u.t0;         // the first own tile, in this split's count
+    u.oa[t] = max(0, min(u.nt, base + (lo - u.kl.lo) / 128));
+    u.ob[t] = max(u.oa[t], min(u.nt, base + (hi - u.kl.lo + 127) / 128));
+  }
+  return true;
+}
+
+}  // namespace area

@@ -177,3 +177,23 @@ def test_workspace_sizes(area):
     assert area.area_sink_attn_ws_bytes(4, 24, 24, 8192, 8192, 128, 2048, 0, 1) == 0
     # the weights' call keeps one score per row and key
     assert area.area_cache_attn_ws_bytes(2, 8, 2, 3, 5000, 128, 1) >= 2 * 8 * 3 * 5000 * 4
+
+
+def test_units_of_the_tensor_core_kernel_cover_what_rows_see(tmp_path):
+    # how work units are cut is integer arithmetic (cache_unit.cuh): checked on
+    # the host over random problems
+    import os
+    import shutil
+    import subprocess
+    from step_adaptive_sparse_b200 import build as b
+    nvcc = b.nvcc()
+    if shutil.which(nvcc) is None and not os.path.exists(nvcc):
+        pytest.skip("nvcc is not available")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "cache_unit_check")
+    subprocess.run([nvcc, "-O2", "-std=c++17", "-Wno-deprecated-gpu-targets", "-I",
+                    os.path.join(root, "include"), "-I", b.CSRC,
+                    os.path.join(root, "tests", "cache_unit_check.cu"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stdout, r.stderr)
+    assert "problems checked" in r.stdout
