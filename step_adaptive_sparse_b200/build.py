@@ -27,19 +27,21 @@ def nvcc() -> str:
 
 # The window instantiations of attn_tc_kernel (template argument WINDOW =
 # true) split their registers with setmaxnreg: 128 threads at 136 and 256 at
-# 184, exactly the allocation of 384 threads at 168.  That holds only if
-# ptxas gives them 168 registers at entry; the host refuses the launch
-# otherwise.  The build checks it here, and that no attention kernel spills.
+# 184, exactly the allocation of 384 threads at 168; cache_tc_kernel does the
+# same.  That holds only if ptxas gives them 168 registers at entry; the host
+# refuses the launch otherwise.  The build checks it here, and that no
+# tensor-core attention kernel spills.
 WINDOW_KERNEL_REGS = 168
+CHECKED = {"attn_tc.cu": "attn_tc_kernel", "cache_tc.cu": "cache_tc_kernel"}
 
 
-def check_attn_resources(ptxas_log: str) -> list[str]:
+def check_attn_resources(ptxas_log: str, kernel: str = "attn_tc_kernel") -> list[str]:
     """Problems found in ptxas -v output for the attention kernels (empty if none)."""
     problems, name, seen = [], None, 0
     for line in ptxas_log.splitlines():
         if "Compiling entry function" in line:
             name = line.split("'")[1] if "'" in line else line
-            if "attn_tc_kernel" not in name:
+            if kernel not in name:
                 name = None
             else:
                 seen += 1
@@ -54,13 +56,13 @@ def check_attn_resources(ptxas_log: str) -> list[str]:
                 problems.append(f"{name}: {stores} bytes spill stores, {loads} bytes spill loads")
         elif "Used" in line and "registers" in line:
             regs = int(line.split("Used")[1].split()[0])
-            window = "attn_tc_kernelILb1E" in name
+            window = kernel == "cache_tc_kernel" or "attn_tc_kernelILb1E" in name
             if window and regs != WINDOW_KERNEL_REGS:
                 problems.append(f"{name}: {regs} registers at entry, the register split needs "
                                 f"{WINDOW_KERNEL_REGS}")
             name = None
     if seen == 0:
-        problems.append("no attn_tc_kernel instantiation in the ptxas output")
+        problems.append(f"no {kernel} instantiation in the ptxas output")
     return problems
 
 
@@ -79,7 +81,7 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
         obj = os.path.join(objdir, src.replace(".cu", ".o"))
         objs.append(obj)
         cmd = common + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if src == "attn_tc.cu" and not verbose:
+        if src in CHECKED and not verbose:
             cmd[1:1] = ["-Xptxas", "-v"]
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
@@ -91,8 +93,8 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
             continue
         if verbose and text:
             print(f"--- {src}\n{text}", file=sys.stderr)
-        if src == "attn_tc.cu":
-            problems = check_attn_resources(text)
+        if src in CHECKED:
+            problems = check_attn_resources(text, CHECKED[src])
             if problems:
                 failed.append((src, "\n".join(problems)))
     if failed:

@@ -84,6 +84,7 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
   __shared__ int s_abort;
   __shared__ __align__(16) Unit s_rec[kRecSlots];
   __shared__ KeySpan s_span[256];          // of the softmax threads' rows
+  __shared__ int s_copied[kStages];        // the stage's tile came by cp.async
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -120,193 +121,192 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
   const uint32_t tmem = s_tmem_base;
   int* abort_flag = &s_abort;
 
-  if (warp < kSoftWarp0)
+  // The paths must not meet between the split and the roles: the compiler then
+  // holds the softmax to the smaller share and spills.
+  if (warp < kSoftWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow) : "memory");
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh) : "memory");
-  if (warp == 0) {
-    // -------------------------------------------------------------- producer
-    uint32_t kv_it = 0, unit_count = 0;
-    bool ok = true;
-    auto publish = [&](uint32_t k) -> bool {
-      const uint32_t slot = k % kRecSlots;
-      if (!warp_wait0(bar(BAR_REC_EMPTY + slot), ((k / kRecSlots) & 1u) ^ 1u, abort_flag))
-        return false;
-      if (lane == 0) {
-        Unit u;
-        u.valid = decode_unit((int)(blockIdx.x + k * gridDim.x), prm, u) ? 1 : 0;
-        s_rec[slot] = u;
-        mbar_arrive(bar(BAR_REC_FULL + slot));
-      }
-      __syncwarp();
-      return true;
-    };
-    ok = publish(0);
-    while (ok) {
-      const Unit& u = s_rec[unit_count % kRecSlots];
-      if (!u.valid) break;
-      if (!(ok = warp_wait0(bar(BAR_Q_EMPTY), (unit_count & 1u) ^ 1u, abort_flag))) break;
-      if (lane == 0) {
-        const int nq = u.r0[1] < prm.rm.RG ? 2 : 1;
-        const uint32_t box = (uint32_t)prm.tile_rows * 128u;    // bytes of a box (64 columns)
-        mbar_arrive_tx(bar(BAR_Q_FULL), nq * G::kHalves * box);
-        for (int t = 0; t < nq; ++t)
-          for (int hf = 0; hf < G::kHalves; ++hf) {
-            const uint32_t dst = sbase + t * G::kTileBytes + hf * kHalfBytes;
-            if (prm.rm.pool_rows)
-              tma_load_3d(dst, &tm.q, bar(BAR_Q_FULL), hf * 64, u.g * prm.rm.pool_rows,
-                          u.r0[t] / prm.rm.pool_rows);
-            else
-              tma_load_3d(dst, &tm.q, bar(BAR_Q_FULL), hf * 64, u.r0[t], u.g);
-          }
-      }
-      __syncwarp();
-      const int nt = u.nt;
-      const int jn = nt < 2 ? nt : 2;         // the next record is published before tile jn
-      bool published = false;
-      for (int j = 0; j < nt && ok; ++j) {
-        if (j == jn) {
-          published = true;
-          if (!(ok = publish(unit_count + 1))) break;
-        }
-        const Tile t = tile_of(u, j);
-        for (int kv = 0; kv < 2; ++kv) {       // K then V
-          const int s = (int)(kv_it % kStages);
-          if (!warp_wait0(bar(BAR_KV_EMPTY + s), ((kv_it / kStages) & 1u) ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t dst = sbase + G::kSmemKV + s * G::kTileBytes;
-          const uint32_t full = bar(BAR_KV_FULL + s);
-          if (t.copy) {
-            // rows past t.n become zeros and are not read
-            const auto* base = static_cast<const __nv_bfloat16*>(kv ? prm.a.v : prm.a.k) +
-                               ((int64_t)u.kvh * prm.a.S + t.j0) * D;
-            constexpr int kChunks = D / 8;              // 16-byte pieces of a row
-            const int q = lane % kChunks;
-#pragma unroll 8
-            for (int r = lane / kChunks; r < 128; r += 32 / kChunks) {
-              const uint32_t at = dst + (uint32_t)((q >> 3) * kHalfBytes + r * 128 +
-                                                   (((q & 7) ^ (r & 7)) << 4));
-              const int rr = r < t.n ? r : 0;
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at),
-                           "l"(base + (int64_t)rr * D + q * 8), "r"(r < t.n ? 16 : 0)
-                           : "memory");
-            }
-            cp_async_arrive(full);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full);
-          } else if (lane == 0) {
-            mbar_arrive_tx(full, G::kTileBytes);
-            const CUtensorMap* map = t.kind ? (kv ? &tm.v : &tm.k) : (kv ? &tm.vp : &tm.kp);
-            for (int hf = 0; hf < G::kHalves; ++hf)
-              tma_load_3d(dst + hf * kHalfBytes, map, full, hf * 64, t.j0, t.kind ? u.kvh : u.ph);
-          }
-          __syncwarp();
-          ++kv_it;
-        }
-      }
-      if (!ok) break;
-      if (!published && !(ok = publish(unit_count + 1))) break;
-      ++unit_count;
-    }
-    // drain: the last load of every stage has landed, no copy is in flight
-    int drain_abort = 0;
-    for (uint32_t k = 0; k < kStages && k < kv_it; ++k) {
-      const uint32_t it = kv_it - 1 - k;
-      warp_wait0(bar(BAR_KV_FULL + it % kStages), (it / kStages) & 1u, &drain_abort);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (warp == 0) {
+      // -------------------------------------------------------------- producer
       uint32_t kv_it = 0, unit_count = 0;
-      uint32_t p_cnt[2] = {0, 0};
       bool ok = true;
-      auto kv_addr = [&](uint32_t it) { return sbase + G::kSmemKV + (it % kStages) * G::kTileBytes; };
-      auto wait_kv = [&](uint32_t it) {
-        return mbar_wait(bar(BAR_KV_FULL + it % kStages), (it / kStages) & 1u, abort_flag);
-      };
-      auto qk = [&](int t, uint32_t ks) {
-        const uint32_t qs = sbase + t * G::kTileBytes, d = tmem + t * 128;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-          mma_ss(d, sdesc(qs + off, 16, 1024), sdesc(ks + off, 16, 1024), kIdescQK, kk > 0);
+      auto publish = [&](uint32_t k) -> bool {
+        const uint32_t slot = k % kRecSlots;
+        if (!warp_wait0(bar(BAR_REC_EMPTY + slot), ((k / kRecSlots) & 1u) ^ 1u, abort_flag))
+          return false;
+        if (lane == 0) {
+          Unit u;
+          u.valid = decode_unit((int)(blockIdx.x + k * gridDim.x), prm, u) ? 1 : 0;
+          s_rec[slot] = u;
+          mbar_arrive(bar(BAR_REC_FULL + slot));
         }
-        mma_commit(bar(BAR_S_FULL0 + t));
-      };
-      auto pv = [&](int t, uint32_t vs, bool first, bool last) -> bool {
-        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * 128;
-        constexpr int kPer = 8 / kPParts;
-#pragma unroll
-        for (int h = 0; h < kPParts; ++h) {
-          if (!mbar_wait(bar((h + 1 < kPParts ? BAR_P_PART0 : BAR_P_FULL0) + t), p_cnt[t] & 1u,
-                         abort_flag))
-            return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = kPer * h; kk < kPer * h + kPer; ++kk)
-            mma_ts(d, p + kk * 8, sdesc(vs + kk * 2048, kHalfBytes, 1024), kIdescPV,
-                   (first && kk == 0) ? 0u : 1u);
-        }
-        ++p_cnt[t];
-        if (last) mma_commit(bar(BAR_O_FULL0 + t));
+        __syncwarp();
         return true;
       };
+      ok = publish(0);
       while (ok) {
-        const uint32_t slot = unit_count % kRecSlots;
-        if (!(ok = mbar_wait(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u, abort_flag)))
-          break;
-        const Unit u = s_rec[slot];
-        mbar_arrive(bar(BAR_REC_EMPTY + slot));
+        const Unit& u = s_rec[unit_count % kRecSlots];
         if (!u.valid) break;
-        if (!(ok = mbar_wait(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
+        if (!(ok = warp_wait0(bar(BAR_Q_EMPTY), (unit_count & 1u) ^ 1u, abort_flag))) break;
+        if (lane == 0) {
+          const int nq = u.r0[1] < prm.rm.RG ? 2 : 1;
+          const uint32_t box = (uint32_t)prm.tile_rows * 128u;    // bytes of a box (64 columns)
+          mbar_arrive_tx(bar(BAR_Q_FULL), nq * G::kHalves * box);
+          for (int t = 0; t < nq; ++t)
+            for (int hf = 0; hf < G::kHalves; ++hf) {
+              const uint32_t dst = sbase + t * G::kTileBytes + hf * kHalfBytes;
+              if (prm.rm.pool_rows)
+                tma_load_3d(dst, &tm.q, bar(BAR_Q_FULL), hf * 64, u.g * prm.rm.pool_rows,
+                            u.r0[t] / prm.rm.pool_rows);
+              else
+                tma_load_3d(dst, &tm.q, bar(BAR_Q_FULL), hf * 64, u.r0[t], u.g);
+            }
+        }
+        __syncwarp();
         const int nt = u.nt;
-        const int f0 = first_tile(u, 0), f1 = first_tile(u, 1);
-        const int l0 = last_tile(u, 0), l1 = last_tile(u, 1);
-        if (nt == 0) mma_commit(bar(BAR_Q_EMPTY));
-        bool copied = false;                       // the coming tile was copied by cp.async
-        if (nt > 0) {
-          if (!(ok = wait_kv(kv_it))) break;
-          copied = tile_of(u, 0).copy;
-          if (copied) fence_proxy_async();
-          tc_fence_after();
-          if (is_active(u, 0, 0)) qk(0, kv_addr(kv_it));
-          if (is_active(u, 1, 0)) qk(1, kv_addr(kv_it));
-          mma_commit(bar(BAR_KV_EMPTY + kv_it % kStages));
-          if (nt == 1) mma_commit(bar(BAR_Q_EMPTY));
-        }
-        for (int j = 0; j < nt; ++j) {
-          const uint32_t vi = kv_it + 2 * j + 1, kn = vi + 1;
-          const bool next = j + 1 < nt;
-          if (!(ok = wait_kv(vi))) break;
-          if (copied) fence_proxy_async();
-          if (is_active(u, 0, j) && !(ok = pv(0, kv_addr(vi), j == f0, j == l0))) break;
-          if (next) {
-            if (!(ok = wait_kv(kn))) break;
-            copied = tile_of(u, j + 1).copy;
-            if (copied) fence_proxy_async();
-            tc_fence_after();
-            if (is_active(u, 0, j + 1)) qk(0, kv_addr(kn));
+        const int jn = nt < 2 ? nt : 2;         // the next record is published before tile jn
+        bool published = false;
+        for (int j = 0; j < nt && ok; ++j) {
+          if (j == jn) {
+            published = true;
+            if (!(ok = publish(unit_count + 1))) break;
           }
-          if (is_active(u, 1, j) && !(ok = pv(1, kv_addr(vi), j == f1, j == l1))) break;
-          mma_commit(bar(BAR_KV_EMPTY + vi % kStages));
-          if (next) {
-            if (is_active(u, 1, j + 1)) qk(1, kv_addr(kn));
-            mma_commit(bar(BAR_KV_EMPTY + kn % kStages));
-            if (j + 2 == nt) mma_commit(bar(BAR_Q_EMPTY));
+          const Tile t = tile_of(u, j);
+          for (int kv = 0; kv < 2; ++kv) {       // K then V
+            const int s = (int)(kv_it % kStages);
+            if (!warp_wait0(bar(BAR_KV_EMPTY + s), ((kv_it / kStages) & 1u) ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            const uint32_t dst = sbase + G::kSmemKV + s * G::kTileBytes;
+            const uint32_t full = bar(BAR_KV_FULL + s);
+            if (lane == 0) s_copied[s] = t.copy;     // read after the stage's barrier
+            if (t.copy) {
+              // rows past t.n become zeros and are not read
+              const auto* base = static_cast<const __nv_bfloat16*>(kv ? prm.a.v : prm.a.k) +
+                                 ((int64_t)u.kvh * prm.a.S + t.j0) * D;
+              constexpr int kChunks = D / 8;              // 16-byte pieces of a row
+              const int q = lane % kChunks;
+  #pragma unroll 8
+              for (int r = lane / kChunks; r < 128; r += 32 / kChunks) {
+                const uint32_t at = dst + (uint32_t)((q >> 3) * kHalfBytes + r * 128 +
+                                                     (((q & 7) ^ (r & 7)) << 4));
+                const int rr = r < t.n ? r : 0;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at),
+                             "l"(base + (int64_t)rr * D + q * 8), "r"(r < t.n ? 16 : 0)
+                             : "memory");
+              }
+              cp_async_arrive(full);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(full);
+            } else if (lane == 0) {
+              mbar_arrive_tx(full, G::kTileBytes);
+              const CUtensorMap* map = t.kind ? (kv ? &tm.v : &tm.k) : (kv ? &tm.vp : &tm.kp);
+              for (int hf = 0; hf < G::kHalves; ++hf)
+                tma_load_3d(dst + hf * kHalfBytes, map, full, hf * 64, t.j0, t.kind ? u.kvh : u.ph);
+            }
+            __syncwarp();
+            ++kv_it;
           }
         }
-        kv_it += 2 * nt;
+        if (!ok) break;
+        if (!published && !(ok = publish(unit_count + 1))) break;
         ++unit_count;
       }
+      // drain: the last load of every stage has landed, no copy is in flight
       int drain_abort = 0;
-      mma_commit(bar(BAR_DRAIN));
-      mbar_wait(bar(BAR_DRAIN), 0, &drain_abort);
+      for (uint32_t k = 0; k < kStages && k < kv_it; ++k) {
+        const uint32_t it = kv_it - 1 - k;
+        warp_wait0(bar(BAR_KV_FULL + it % kStages), (it / kStages) & 1u, &drain_abort);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        uint32_t kv_it = 0, unit_count = 0;
+        uint32_t p_cnt[2] = {0, 0};
+        bool ok = true;
+        auto kv_addr = [&](uint32_t it) { return sbase + G::kSmemKV + (it % kStages) * G::kTileBytes; };
+        auto wait_kv = [&](uint32_t it) {
+          if (!mbar_wait(bar(BAR_KV_FULL + it % kStages), (it / kStages) & 1u, abort_flag))
+            return false;
+          if (s_copied[it % kStages]) fence_proxy_async();
+          return true;
+        };
+        auto qk = [&](int t, uint32_t ks) {
+          const uint32_t qs = sbase + t * G::kTileBytes, d = tmem + t * 128;
+  #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+            mma_ss(d, sdesc(qs + off, 16, 1024), sdesc(ks + off, 16, 1024), kIdescQK, kk > 0);
+          }
+          mma_commit(bar(BAR_S_FULL0 + t));
+        };
+        auto pv = [&](int t, uint32_t vs, bool first, bool last) -> bool {
+          const uint32_t d = tmem + 256 + t * 128, p = tmem + t * 128;
+          constexpr int kPer = 8 / kPParts;
+  #pragma unroll
+          for (int h = 0; h < kPParts; ++h) {
+            if (!mbar_wait(bar((h + 1 < kPParts ? BAR_P_PART0 : BAR_P_FULL0) + t), p_cnt[t] & 1u,
+                           abort_flag))
+              return false;
+            tc_fence_after();
+  #pragma unroll
+            for (int kk = kPer * h; kk < kPer * h + kPer; ++kk)
+              mma_ts(d, p + kk * 8, sdesc(vs + kk * 2048, kHalfBytes, 1024), kIdescPV,
+                     (first && kk == 0) ? 0u : 1u);
+          }
+          ++p_cnt[t];
+          if (last) mma_commit(bar(BAR_O_FULL0 + t));
+          return true;
+        };
+        while (ok) {
+          const uint32_t slot = unit_count % kRecSlots;
+          if (!(ok = mbar_wait(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u, abort_flag)))
+            break;
+          const Unit& u = s_rec[slot];
+          if (!u.valid) break;
+          const int nt = u.nt;
+          const TileRange a0 = tile_range(u, 0), a1 = tile_range(u, 1);
+          mbar_arrive(bar(BAR_REC_EMPTY + slot));
+          if (!(ok = mbar_wait(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
+          if (nt == 0) mma_commit(bar(BAR_Q_EMPTY));
+          if (nt > 0) {
+            if (!(ok = wait_kv(kv_it))) break;
+            tc_fence_after();
+            if (a0.has(0)) qk(0, kv_addr(kv_it));
+            if (a1.has(0)) qk(1, kv_addr(kv_it));
+            mma_commit(bar(BAR_KV_EMPTY + kv_it % kStages));
+            if (nt == 1) mma_commit(bar(BAR_Q_EMPTY));
+          }
+          for (int j = 0; j < nt; ++j) {
+            const uint32_t vi = kv_it + 2 * j + 1, kn = vi + 1;
+            const bool next = j + 1 < nt;
+            if (!(ok = wait_kv(vi))) break;
+            if (a0.has(j) && !(ok = pv(0, kv_addr(vi), j == a0.first, j == a0.last))) break;
+            if (next) {
+              if (!(ok = wait_kv(kn))) break;
+              tc_fence_after();
+              if (a0.has(j + 1)) qk(0, kv_addr(kn));
+            }
+            if (a1.has(j) && !(ok = pv(1, kv_addr(vi), j == a1.first, j == a1.last))) break;
+            mma_commit(bar(BAR_KV_EMPTY + vi % kStages));
+            if (next) {
+              if (a1.has(j + 1)) qk(1, kv_addr(kn));
+              mma_commit(bar(BAR_KV_EMPTY + kn % kStages));
+              if (j + 2 == nt) mma_commit(bar(BAR_Q_EMPTY));
+            }
+          }
+          kv_it += 2 * nt;
+          ++unit_count;
+        }
+        int drain_abort = 0;
+        mma_commit(bar(BAR_DRAIN));
+        mbar_wait(bar(BAR_DRAIN), 0, &drain_abort);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= kSoftWarp0) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh) : "memory");
     // ------------------------------------------------------ softmax / epilogue
     const int qt = (warp - kSoftWarp0) >> 2;
     const int trow = ((warp & 3) << 5) + lane;       // TMEM lane = row of the tile
@@ -335,34 +335,41 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
         }
         s_span[qt * 128 + trow] = sp;
       }
-      const int nt = u.nt, first = first_tile(u, qt), last = last_tile(u, qt);
+      // tiles that every row of the warp sees whole: keys [max lo, min hi)
+      const int wlo = __reduce_max_sync(0xffffffffu, s_span[qt * 128 + trow].lo);
+      const int whi = __reduce_min_sync(0xffffffffu, s_span[qt * 128 + trow].hi);
+      const int first = first_tile(u, qt), last = last_tile(u, qt), lead = u.lead[qt];
+      uint32_t whole = 0;                      // of 32 tiles, one bit each
+      int at32 = INT_MIN / 2;                  // the first of them
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < nt; ++j) {
-        if (!is_active(u, qt, j)) continue;
-        // keys [ka, kb) and [0, kc) of the tile are this row's
-        int ka, kb, kc = 0;
-        {
-          const Tile t = tile_of(u, j);
-          const KeySpan sp = s_span[qt * 128 + trow];
-          if (t.kind == 0) {
-            ka = 0;
-            kb = sees_prefix(prm.a, sp) ? t.n : 0;
-          } else {
-            ka = max(sp.lo - t.j0, 0);
-            kb = min(sp.hi - t.j0, t.n);
-            kc = min(prm.a.sinks - t.j0, kb);
-          }
+      for (int j = first; j <= last;) {
+        if (j - at32 >= 32) {
+          at32 = j;
+          const Tile t = tile_of(u, min(j + lane, u.nt - 1));
+          whole = __ballot_sync(0xffffffffu, t.n == 128 && (t.kind == 0 ? !prm.a.causal || whi > 0
+                                                                        : whi >= t.j0 + 128 &&
+                                             (wlo <= t.j0 || prm.a.sinks >= t.j0 + 128)));
         }
-        const bool masked = __any_sync(0xffffffffu, !((ka == 0 && kb >= 128) || kc >= 128));
-        const bool heads = __any_sync(0xffffffffu, kc > 0);
+        const bool masked = !(whole >> (j - at32) & 1u);
         if (!(ok = warp_wait_all(bar(BAR_S_FULL0 + qt), s_cnt & 1u, abort_flag))) break;
         ++s_cnt;
         tc_fence_after();
         uint32_t sr[128];
         tmem_ld128(tS, sr);
         if (masked) {
+          // keys [ka, kb) and [0, kc) of the tile are this row's
+          const Tile t = tile_of(u, j);
+          const KeySpan sp = s_span[qt * 128 + trow];
+          int ka = 0, kb, kc = 0;
+          if (t.kind == 0) {
+            kb = sees_prefix(prm.a, sp) ? t.n : 0;
+          } else {
+            ka = max(sp.lo - t.j0, 0);
+            kb = min(sp.hi - t.j0, t.n);
+            kc = min(prm.a.sinks - t.j0, kb);
+          }
           const unsigned width = kb > ka ? (unsigned)(kb - ka) : 0u;
-          if (heads) {
+          if (__any_sync(0xffffffffu, kc > 0)) {
 #pragma unroll
             for (int i = 0; i < 128; ++i)
               if ((unsigned)(i - ka) >= width && i >= kc) sr[i] = 0xff800000u;
@@ -419,6 +426,7 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
           mbar_arrive(bar((h + 1 < kPParts ? BAR_P_PART0 : BAR_P_FULL0) + qt));
         }
         l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        j = next_tile(j, lead, u.oa[qt]);
       }
       if (!ok) break;
       // ---- epilogue

@@ -64,9 +64,27 @@ __host__ __device__ __forceinline__ bool is_active(const Unit& u, int t, int j) 
   return j < u.lead[t] || (j >= u.oa[t] && j < u.ob[t]);
 }
 // First and last tile of a row tile; last < 0: it has none.
-__host__ __device__ __forceinline__ int first_tile(const Unit& u, int t) { return u.lead[t] > 0 ? 0 : u.oa[t]; }
+__host__ __device__ __forceinline__ int first_tile(const Unit& u, int t) {
+  return u.lead[t] > 0 ? 0 : u.oa[t];
+}
 __host__ __device__ __forceinline__ int last_tile(const Unit& u, int t) {
   return u.ob[t] > u.oa[t] ? u.ob[t] - 1 : u.lead[t] - 1;
+}
+
+// The tile after j of a row tile's tiles, first_tile() to last_tile().
+__host__ __device__ __forceinline__ int next_tile(int j, int lead, int oa) {
+  return j + 1 == lead ? oa : j + 1;
+}
+
+// The tiles of a row tile, in registers.
+struct TileRange {
+  int lead, oa, ob, first, last;
+  __host__ __device__ __forceinline__ bool has(int j) const {
+    return j < lead || (j >= oa && j < ob);
+  }
+};
+__host__ __device__ __forceinline__ TileRange tile_range(const Unit& u, int t) {
+  return TileRange{u.lead[t], u.oa[t], u.ob[t], first_tile(u, t), last_tile(u, t)};
 }
 
 // Unit idx of a launch; false behind the last one.
@@ -110,7 +128,7 @@ __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& 
     u.lead[t] = u.oa[t] = u.ob[t] = 0;
     const int ra = u.r0[t], rz = t == 0 ? u.r0[1] : r1;
     if (ra >= rz) continue;                      // no rows
-    u.lead[t] = max(0, min(u.nt, u.tp + u.ts - u.t0));
+    u.lead[t] = u.oa[t] = u.ob[t] = max(0, min(u.nt, u.tp + u.ts - u.t0));
     if (to == 0) continue;
     int i0, i1;
     query_range(a, ra, rz, i0, i1);
@@ -118,7 +136,7 @@ __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& 
     int lo = key_span(a, len, i0).lo;
     const int hi = key_span(a, len, i1).hi;
     if (hi <= lo) {                              // padding rows alone: nothing to see
-      u.lead[t] = 0;
+      u.lead[t] = u.oa[t] = u.ob[t] = 0;
       continue;
     }
     if (a.sinks > u.kl.lo) lo = u.kl.lo;         // sinks among the first own tiles

@@ -45,6 +45,12 @@ static int check(const CacheArgs& a, const CacheRows& rm, int nsplit) {
           if (n++ == 0 && j != first) return printf("first tile\n"), 1;
           if (j > last) return printf("last tile\n"), 1;
         }
+        // the softmax warps' walk takes exactly these tiles, in order
+        int m = 0;
+        for (int j = first, before = -1; j <= last; j = next_tile(j, u.lead[t], u.oa[t]), ++m)
+          if (j <= before || !is_active(u, t, j)) return printf("walk takes tile %d\n", j), 1;
+          else before = j;
+        if (m != n) return printf("walk of %d tiles, not %d\n", m, n), 1;
         if ((n == 0) != (last < 0)) return printf("no tile, last %d\n", last), 1;
         if (n && !is_active(u, t, last)) return printf("last tile inactive\n"), 1;
         for (int r = u.r0[t]; r < std::min(u.r0[t] + p.tile_rows, rm.RG); ++r) {

@@ -197,3 +197,14 @@ def test_units_of_the_tensor_core_kernel_cover_what_rows_see(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, (r.returncode, r.stdout, r.stderr)
     assert "problems checked" in r.stdout
+
+
+def test_build_checks_the_tensor_core_kernel():
+    from step_adaptive_sparse_b200 import build as b
+    log = "\n".join(["ptxas info    : Compiling entry function '_ZN4area15cache_tc_kernelILi128EEEv' for 'sm_100a'",
+                     "    0 bytes stack frame, %d bytes spill stores, 0 bytes spill loads",
+                     "ptxas info    : Used %d registers, used 1 barriers"])
+    assert b.check_attn_resources(log % (0, 168), "cache_tc_kernel") == []
+    assert len(b.check_attn_resources(log % (0, 160), "cache_tc_kernel")) == 1
+    assert len(b.check_attn_resources(log % (8, 168), "cache_tc_kernel")) == 1
+    assert len(b.check_attn_resources(log % (0, 168))) == 1
