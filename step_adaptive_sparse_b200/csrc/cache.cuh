@@ -48,12 +48,15 @@ struct CacheRows {
 // Where a launch leaves its results.
 struct CacheOut {
   int nsplit;        // splits of this launch
+  int cluster;       // splits that one cluster joins; the others' slots hold one split
   int slot0;         // its first slot in part_o / part_ml
   int direct;        // 1: one split in all, the output is written to o
   float* part_o;     // [slots][rows][D]
   float2* part_ml;   // [slots][rows] (m, l)
   float* logits;     // [rows][S] scores in log2 units, or null
   int64_t rows;      // B * H * Nq
+  const float* acc;  // with a direct launch that has scores: the weights' sums
+  float* acco;
 };
 
 __host__ __device__ __forceinline__ int cache_len(const CacheArgs& a, int b) {
@@ -148,15 +151,15 @@ __host__ __device__ __forceinline__ KeyList key_list(const CacheArgs& a, const C
 // ---- host side ------------------------------------------------------------
 enum { CACHE_OP_SINK, CACHE_OP_PREFIX, CACHE_OP_WEIGHTS };
 
-// The kernels: CUDA cores with 16 or 64 rows to a block, the one for few rows,
-// the tensor-core one.
-enum { CACHE_SIMT16, CACHE_SIMT64, CACHE_DEC, CACHE_TC };
+// The kernels: for few rows, for many rows in fp32 and in bf16.
+enum { CACHE_DEC, CACHE_SIMT, CACHE_TC };
 // A launch of a call: the kernel, the rows and the splits of their keys.
 struct CacheLaunch {
   bool used;
   int kernel;
   CacheRows rows;
   int nsplit;
+  int cluster;
 };
 // The launches of a call and the layout of its workspace; cache_plan computes
 // them from the sizes alone.
@@ -170,9 +173,11 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
                int dtype, CachePlan* p);
 
 cudaError_t launch_cache_simt(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
-                              int dtype, bool wide, cudaStream_t s);
-cudaError_t launch_cache_dec(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
-                             cudaStream_t s);
+                              cudaStream_t s);
+cudaError_t launch_cache_dec_bf16(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
+                                  cudaStream_t s);
+cudaError_t launch_cache_dec_f32(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
+                                 cudaStream_t s);
 // Joins `slots` partial results per row into o, and their log2-sum-exp into
 // lse when that is given.
 cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const float2* part_ml,

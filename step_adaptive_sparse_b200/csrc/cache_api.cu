@@ -9,16 +9,19 @@ namespace {
 
 constexpr int64_t kSms = 148;        // B200; the workspace's size may not hang on the device
 
+constexpr int64_t kPoolBytes = 32 << 20;
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t ceil256(int64_t n) { return (n + 255) & ~int64_t(255); }
 
 // Rows that one work item of a kernel takes.
-int rows_per_block(int kernel, const CacheRows& rm) {
+int rows_per_block(int kernel, int dtype, const CacheRows& rm) {
   switch (kernel) {
     case CACHE_TC: return 2 * tc_tile_rows(rm);
-    case CACHE_SIMT64: return 64;
-    case CACHE_DEC: return rm.RG <= 8 ? 8 : 16;
-    default: return 16;
+    case CACHE_SIMT: return 64;
+    default:
+      if (dtype == AREA_DTYPE_BF16) return rm.RG <= 8 ? 8 : 16;
+      return rm.RG <= 2 ? 2 : rm.RG <= 4 ? 4 : 8;
   }
 }
 
@@ -44,19 +47,31 @@ int tc_splits(int64_t units, int64_t keys, int64_t rows, int D) {
 void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D) {
   const int RG = l.rows.RG;
   l.used = true;
-  if (dtype == AREA_DTYPE_BF16)
-    l.kernel = RG <= 16 || op == CACHE_OP_WEIGHTS ? CACHE_DEC : CACHE_TC;
+  l.cluster = 1;
+  if (RG <= 16 || (op == CACHE_OP_WEIGHTS && dtype == AREA_DTYPE_BF16))
+    l.kernel = CACHE_DEC;
   else
-    l.kernel = RG <= 16 ? CACHE_SIMT16 : CACHE_SIMT64;
-  const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, l.rows));
+    l.kernel = dtype == AREA_DTYPE_BF16 ? CACHE_TC : CACHE_SIMT;
+  const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, dtype, l.rows));
   int64_t n;
   if (l.kernel == CACHE_TC) {
     n = tc_splits(blocks, keys, rows, D);
   } else if (l.kernel == CACHE_DEC) {
-    // eight rounds of four blocks on each SM, so that the last round is a small
-    // share, with 512 keys to a split; where that leaves SMs idle, 128
-    n = std::min(cdiv(32 * kSms, blocks), cdiv(keys, 512));
-    if (blocks * n < 2 * kSms) n = std::min(cdiv(2 * kSms, blocks), cdiv(keys, 128));
+    const int resident = (dtype == AREA_DTYPE_BF16 ? 3 : 2) * (int)kSms;
+    if (blocks * 8 <= resident && (keys <= 4096 || blocks * 8 >= 2 * kSms)) {
+      // All blocks run at once: a cluster of up to 8 joins its splits itself
+      // (8 sequences' tokens of 500 keys: 6.0 us, with a join launch 7.1).  In
+      // larger grids the blocks of a cluster wait for room together (512 heads
+      // of 4100 keys in 8 splits: 214 us, without clusters 186).
+      while (l.cluster < 8 && l.cluster * 128 < keys) l.cluster *= 2;
+      n = l.cluster;
+    } else {
+      // 1024 keys to a split, which starting a block costs little of (the same
+      // heads in 4 splits: 172 us, in 8: 186, in 2: 185), and at most eight
+      // rounds; where that leaves SMs idle, 128 keys
+      n = std::min(cdiv(32 * kSms, blocks), (keys + 512) / 1024);
+      if (blocks * n < 2 * kSms) n = std::min(cdiv(2 * kSms, blocks), cdiv(keys, 128));
+    }
   } else {
     // four blocks on each SM, at least two tiles of 64 keys to a split
     n = std::min(cdiv(4 * kSms, blocks), cdiv(keys, 128));
@@ -86,7 +101,11 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   p->rows = (int64_t)B * H * Nq;
   if (p->rows > INT_MAX) return AREA_EUNSUPPORTED;
   const int R = H / Hk * Nq;
-  const bool pool = op == CACHE_OP_PREFIX && P > 0 && B > 1 && R < 64;
+  // Few rows of a sequence: the prefix against the rows of all sequences, once
+  // it is so large that reading it from L2 for each costs more than the second
+  // launch and the join.
+  const int64_t pre = (int64_t)B * Hk * P * D * (dtype == AREA_DTYPE_BF16 ? 4 : 8);
+  const bool pool = op == CACHE_OP_PREFIX && P > 0 && B > 1 && R < 64 && pre > kPoolBytes;
   p->pooled = CacheLaunch{};
   CacheLaunch& m = p->main;
   m = CacheLaunch{};
@@ -98,17 +117,22 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   int64_t own = (int64_t)sinks + window + (per_head ? 256 : Nq);
   if (own > S) own = S;
   if (!pool || S > 0) cut(m, op, dtype, own + (m.rows.use_prefix ? P : 0), p->rows, D);
-  p->slots = m.used ? m.nsplit : 0;
+  p->slots = m.used ? m.nsplit / m.cluster : 0;
   if (pool) {
     p->pooled.rows = CacheRows{B * R, Hk, 1, R, 1, 0};
     cut(p->pooled, op, dtype, P, p->rows, D);
-    p->slots += p->pooled.nsplit;
+    p->slots += p->pooled.nsplit / p->pooled.cluster;
   }
-  if (p->slots == 1 && op != CACHE_OP_WEIGHTS) p->slots = 0;
+  // The scores' softmax needs the whole row's sum: the kernel for few rows has
+  // it when one block or cluster has all of a key head's rows and splits.
+  const bool whole = op != CACHE_OP_WEIGHTS ||
+                     (m.kernel == CACHE_DEC &&
+                      m.rows.RG <= rows_per_block(CACHE_DEC, dtype, m.rows) && m.rows.kv_div == 1);
+  if (p->slots == 1 && whole) p->slots = 0;
   p->off_ml = 0;
   p->off_o = p->off_ml + ceil256(p->slots * p->rows * 8);
   p->off_lse = p->off_o + ceil256(p->slots * p->rows * D * 4);
-  p->off_logits = p->off_lse + (op == CACHE_OP_WEIGHTS ? ceil256(p->rows * 4) : 0);
+  p->off_logits = p->off_lse + (op == CACHE_OP_WEIGHTS && p->slots ? ceil256(p->rows * 4) : 0);
   p->bytes = p->off_logits + (op == CACHE_OP_WEIGHTS ? ceil256(p->rows * S * 4) : 0);
   const int64_t blocks = cdiv(m.rows.RG, 8) * m.rows.groups * std::max(m.nsplit, 1);
   if (blocks > INT_MAX || cdiv(S, 256) * B * Hk > INT_MAX) return AREA_EUNSUPPORTED;
@@ -141,19 +165,26 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     out.part_ml = reinterpret_cast<float2*>(w + p.off_ml);
     out.part_o = reinterpret_cast<float*>(w + p.off_o);
   }
-  if (op == CACHE_OP_WEIGHTS) out.logits = reinterpret_cast<float*>(w + p.off_logits);
+  if (op == CACHE_OP_WEIGHTS) {
+    out.logits = reinterpret_cast<float*>(w + p.off_logits);
+    out.acc = acc;
+    out.acco = acco;
+  }
   cudaError_t e;
   const CacheLaunch* ls[2] = {&p.main, &p.pooled};
   for (const CacheLaunch* l : ls) {
     if (!l->used) continue;
     out.nsplit = l->nsplit;
-    e = l->kernel == CACHE_DEC
-            ? launch_cache_dec(a, l->rows, out, s)
-        : l->kernel == CACHE_TC
-            ? launch_cache_tc(a, l->rows, out, s)
-            : launch_cache_simt(a, l->rows, out, dtype, l->kernel == CACHE_SIMT64, s);
+    out.cluster = l->cluster;
+    switch (l->kernel) {
+      case CACHE_TC: e = launch_cache_tc(a, l->rows, out, s); break;
+      case CACHE_SIMT: e = launch_cache_simt(a, l->rows, out, s); break;
+      default:
+        e = dtype == AREA_DTYPE_BF16 ? launch_cache_dec_bf16(a, l->rows, out, s)
+                                     : launch_cache_dec_f32(a, l->rows, out, s);
+    }
     if (e != cudaSuccess) return fail_cuda(e);
-    out.slot0 += l->nsplit;
+    out.slot0 += l->nsplit / l->cluster;
   }
   if (!p.slots) return AREA_OK;
   float* lse = op == CACHE_OP_WEIGHTS ? reinterpret_cast<float*>(w + p.off_lse) : nullptr;

@@ -18,14 +18,13 @@
 // the result is exact); the weights are rounded once, to bf16, for the second
 // product.  mma.sync is enough here: at 8 rows the products take a fifth of
 // the time that the keys take to arrive.
-#include "cache.cuh"
+#include "cache_dec.cuh"
 
 namespace area {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kStep = 16;                    // keys of a warp and step
-constexpr int kTile = kWarps * kStep;        // keys of a block and step
+constexpr int kTile = kDecWarps * kStep;        // keys of a block and step
 constexpr float kSlack = 8.f;                // log2 units
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -45,11 +44,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Keys and values are read once: they need no place in L1.
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
   uint4 v;
@@ -60,17 +54,14 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, (D == 64 ? 5 : 4) - NT)
+__global__ void __launch_bounds__(kDecWarps * 32, (D == 64 ? 5 : 4) - NT)
 cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int nrb) {
   constexpr int kRows = 8 * NT;
   constexpr int kU = D / 32;                 // 16-byte loads of a thread per key row
   constexpr int kG = D / 64;                 // 16-byte loads of a thread per value row
-  __shared__ int64_t s_row[kRows];
-  __shared__ KeySpan s_span[kRows];
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-  __shared__ __align__(16) float s_o[kWarps][kRows][D];
+  __shared__ DecSmem<D, kRows> sm;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = lane >> 2, c = lane & 3;
   const int sp = blockIdx.x % out.nsplit;
   const int rb = blockIdx.x / out.nsplit % nrb;
@@ -84,18 +75,7 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
   const auto* kpb = static_cast<const __nv_bfloat16*>(a.kp) + pbase;
   const auto* vpb = static_cast<const __nv_bfloat16*>(a.vp) + pbase;
 
-  if (tid < kRows) {
-    KeySpan s{0, 0};
-    int64_t row = -1;
-    if (r0 + tid < r1) {
-      const CacheRow cr = cache_row(a, rm, g, r0 + tid);
-      row = cr.row;
-      s = key_span(a, cache_len(a, cr.b), cr.i);
-    }
-    s_row[tid] = row;
-    s_span[tid] = s;
-  }
-  __syncthreads();
+  dec_rows(sm, a, rm, g, r0);
 
   // this split's tiles of kTile keys
   const int ntile = (kl.total + kTile - 1) / kTile;
@@ -142,7 +122,7 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
   uint32_t qf[NT][kU][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int64_t row = s_row[8 * t + n];
+    const int64_t row = sm.row[8 * t + n];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       uint4 x = make_uint4(0, 0, 0, 0);
@@ -160,9 +140,9 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int r = 8 * t + 2 * c + x;
-      span[t][x] = s_span[r];
-      pre[t][x] = s_row[r] >= 0 && sees_prefix(a, span[t][x]);
-      if (s_row[r] >= 0)
+      span[t][x] = sm.span[r];
+      pre[t][x] = sm.row[r] >= 0 && sees_prefix(a, span[t][x]);
+      if (sm.row[r] >= 0)
         all = all && (kl.np == 0 || pre[t][x]) &&
               (kl.total == kl.np ||
                (span[t][x].hi - kl.lo == kl.total - kl.np - kl.ns && span[t][x].lo == kl.lo));
@@ -205,7 +185,7 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
           const int key = w < kl.ns ? w : kl.lo + (w - kl.ns);
           const bool in = u < uend && (u < kl.np ? pre[t][x & 1] : sees_own(a, span[t][x & 1], key));
           if (out.logits && in) {
-            const int64_t row = s_row[8 * t + 2 * c + (x & 1)];
+            const int64_t row = sm.row[8 * t + 2 * c + (x & 1)];
             if (row >= 0) out.logits[row * a.S + key] = s[t][x];
           }
           if (!in) s[t][x] = -INFINITY;
@@ -270,59 +250,28 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
 #pragma unroll
       for (int y = 4; y < 32; y <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], y);
       if (n == 0) {
-        s_m[warp][r] = m[t][x];
-        s_l[warp][r] = l[t][x];
+        sm.m[warp][r] = m[t][x];
+        sm.l[warp][r] = l[t][x];
       }
 #pragma unroll
       for (int i = 0; i < kG * 4; ++i)
-        *reinterpret_cast<float2*>(&s_o[warp][r][64 * (i >> 2) + 8 * n + 2 * (i & 3)]) =
+        *reinterpret_cast<float2*>(&sm.o[warp][r][64 * (i >> 2) + 8 * n + 2 * (i & 3)]) =
             make_float2(o[t][i][x], o[t][i][x + 2]);
     }
-  __syncthreads();
-  constexpr int kPer = 4;                    // columns of a thread
-  for (int e = tid; e < kRows * (D / kPer); e += kWarps * 32) {
-    const int r = e / (D / kPer), d = e % (D / kPer) * kPer;
-    const int64_t row = s_row[r];
-    if (row < 0) continue;
-    float mm = s_m[0][r];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f, f[kPer] = {};
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float al = ex2(s_m[w][r] - ref);
-      ll = fmaf(al, s_l[w][r], ll);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) f[i] = fmaf(al, s_o[w][r][d + i], f[i]);
-    }
-    if (out.direct) {
-      const float inv = ll == 0.f ? 0.f : 1.f / ll;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) f[i] = ll == 0.f ? 0.f : f[i] * inv;
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * D + d) =
-          make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
-    } else {
-      const int64_t at = (int64_t)(out.slot0 + sp) * out.rows + row;
-      if (d == 0) out.part_ml[at] = make_float2(mm, ll);
-      if (ll != 0.f)
-        *reinterpret_cast<float4*>(out.part_o + at * D + d) = make_float4(f[0], f[1], f[2], f[3]);
-    }
-  }
+  dec_finish<__nv_bfloat16>(sm, a, out, sp, kvh, t0 * kTile, uend);
 }
 
 template <int D, int NT>
 cudaError_t launch(const CacheArgs& a, const CacheRows& rm, const CacheOut& out, cudaStream_t s) {
   const int nrb = (rm.RG + 8 * NT - 1) / (8 * NT);
   const int64_t grid = (int64_t)rm.groups * nrb * out.nsplit;
-  cache_dec_kernel<D, NT><<<(unsigned)grid, kWarps * 32, 0, s>>>(a, rm, out, nrb);
-  return cudaGetLastError();
+  return launch_dec(cache_dec_kernel<D, NT>, grid, a, rm, out, nrb, s);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_dec(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
-                             cudaStream_t s) {
+cudaError_t launch_cache_dec_bf16(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
+                                  cudaStream_t s) {
   if (rm.RG <= 8) return a.D == 64 ? launch<64, 1>(a, rm, out, s) : launch<128, 1>(a, rm, out, s);
   return a.D == 64 ? launch<64, 2>(a, rm, out, s) : launch<128, 2>(a, rm, out, s);
 }

@@ -46,24 +46,41 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const float* __restrict
   if (lse && threadIdx.x == 0) lse[row] = total == 0.f ? INFINITY : ref + log2f(total);
 }
 
-// One thread per key of a key head; its rows' weights are added in order.
-__global__ void __launch_bounds__(256) cache_weights_kernel(const CacheArgs a,
-                                                            const float* __restrict__ logits,
-                                                            const float* __restrict__ lse,
-                                                            const float* acc, float* acco,
-                                                            int chunks) {
+// kWKeys keys of a key head to a thread, a block apart; a key's rows' weights
+// are added in order.
+constexpr int kWThreads = 128, kWKeys = 4;
+__global__ void __launch_bounds__(kWThreads) cache_weights_kernel(const CacheArgs a,
+                                                                  const float* __restrict__ logits,
+                                                                  const float* __restrict__ lse,
+                                                                  const float* acc, float* acco,
+                                                                  int chunks) {
   const int kvh = blockIdx.x / chunks;                       // (b, key head)
-  const int j = blockIdx.x % chunks * 256 + threadIdx.x;
-  if (j >= a.S) return;
+  const int j0 = blockIdx.x % chunks * (kWThreads * kWKeys) + threadIdx.x;
   const int len = cache_len(a, kvh / a.Hk);
   const int R = a.H / a.Hk * a.Nq;
-  const int64_t row0 = (int64_t)kvh * R;
-  float sum = 0.f;
-  if (j < len)
-    for (int r = 0; r < R; ++r)
-      if (j <= len - a.Nq + r % a.Nq) sum += exp2f(logits[(row0 + r) * a.S + j] - lse[row0 + r]);
-  const int64_t at = (int64_t)kvh * a.S + j;
-  acco[at] = (acc ? acc[at] : 0.f) + sum;
+  const int64_t row0 = (int64_t)kvh * R, at = (int64_t)kvh * a.S;
+  float sum[kWKeys] = {}, old[kWKeys];
+#pragma unroll
+  for (int x = 0; x < kWKeys; ++x) {
+    const int j = j0 + x * kWThreads;
+    old[x] = acc && j < a.S ? acc[at + j] : 0.f;
+  }
+  int i = 0;
+#pragma unroll 4
+  for (int r = 0; r < R; ++r) {
+    const int end = len - a.Nq + 1 + i;                      // the row sees keys below it
+    const float z = lse[row0 + r];
+    const float* src = logits + (row0 + r) * a.S + j0;
+#pragma unroll
+    for (int x = 0; x < kWKeys; ++x)
+      if (j0 + x * kWThreads < end) sum[x] += exp2f(src[x * kWThreads] - z);
+    if (++i == a.Nq) i = 0;
+  }
+#pragma unroll
+  for (int x = 0; x < kWKeys; ++x) {
+    const int j = j0 + x * kWThreads;
+    if (j < a.S) acco[at + j] = old[x] + sum[x];
+  }
 }
 
 }  // namespace
@@ -85,9 +102,9 @@ cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const flo
 
 cudaError_t launch_cache_weights(const CacheArgs& a, const float* logits, const float* lse,
                                  const float* acc, float* acco, cudaStream_t s) {
-  const int chunks = (a.S + 255) / 256;
-  cache_weights_kernel<<<(unsigned)((int64_t)a.B * a.Hk * chunks), 256, 0, s>>>(a, logits, lse, acc,
-                                                                               acco, chunks);
+  const int per = kWThreads * kWKeys, chunks = (a.S + per - 1) / per;
+  cache_weights_kernel<<<(unsigned)((int64_t)a.B * a.Hk * chunks), kWThreads, 0, s>>>(
+      a, logits, lse, acc, acco, chunks);
   return cudaGetLastError();
 }
 

@@ -30,16 +30,6 @@ __device__ __forceinline__ void load_vec(const float* p, float (&f)[4]) {
   const float4 t = *reinterpret_cast<const float4*>(p);
   f[0] = t.x, f[1] = t.y, f[2] = t.z, f[3] = t.w;
 }
-__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 t = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
 template <int W>
 __device__ __forceinline__ void lds(const float* p, float (&f)[W]) {
   if constexpr (W == 4) {
@@ -252,19 +242,11 @@ cudaError_t launch(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_t(const CacheArgs& a, const CacheRows& rm, const CacheOut& out, bool wide,
-                     cudaStream_t s) {
-  if (a.D == 64) return wide ? launch<T, 64, 64>(a, rm, out, s) : launch<T, 64, 16>(a, rm, out, s);
-  return wide ? launch<T, 128, 64>(a, rm, out, s) : launch<T, 128, 16>(a, rm, out, s);
-}
-
 }  // namespace
 
 cudaError_t launch_cache_simt(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
-                              int dtype, bool wide, cudaStream_t s) {
-  if (dtype == AREA_DTYPE_F32) return launch_t<float>(a, rm, out, wide, s);
-  return launch_t<__nv_bfloat16>(a, rm, out, wide, s);
+                              cudaStream_t s) {
+  return a.D == 64 ? launch<float, 64, 64>(a, rm, out, s) : launch<float, 128, 64>(a, rm, out, s);
 }
 
 }  // namespace area

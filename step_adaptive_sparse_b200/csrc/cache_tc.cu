@@ -391,7 +391,10 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
 #pragma unroll
           for (int q = 0; q < t; ++q) pm[q] = fmaxf(pm[q], pm[q + t]);
         const float mnew = fmaxf(pm[0] * sl2, m);
-        const bool rescale = j > first && __any_sync(0xffffffffu, mnew > m + kRescaleThreshold);
+        // rows that do not exist hold what the tile last held: they have no say, or
+        // the real rows' rounding would hang on it
+        const bool rescale =
+            j > first && __any_sync(0xffffffffu, rvalid && mnew > m + kRescaleThreshold);
         const float alpha = rescale ? (m == -INFINITY ? 0.f : fast_exp2(m - mnew)) : 1.f;
         if (j == first || rescale) m = mnew;
         l *= alpha;

@@ -127,7 +127,8 @@ def test_sink_refusals(area, change, status):
 @pytest.mark.parametrize("change,status", ATTN + [
     ({"kp": None}, EINVAL), ({"vp": None}, EINVAL), ({"kp": A + 8}, EINVAL), ({"P": -1}, EINVAL),
     ({"causal": 2}, EINVAL), ({"causal": -1}, EINVAL), ({"P": 0, "S": 0}, EINVAL),
-    ({"P": 1 << 30, "S": 1 << 30}, EUNSUPPORTED), ({"nb": 0}, ENOSPACE), ({"ws": None}, EINVAL)])
+    ({"P": 1 << 30, "S": 1 << 30}, EUNSUPPORTED), ({"P": 100000, "nb": 16}, ENOSPACE),
+    ({"P": 100000, "ws": None}, EINVAL)])
 def test_prefix_refusals(area, change, status):
     with pytest.raises(area.AreaError) as e:
         prefix(area, **change)

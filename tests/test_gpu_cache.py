@@ -241,6 +241,11 @@ PREFIX = [
     (3, 4, 2, 2, 0, 100, 64, [100, 1, 50]),
     (1, 4, 2, 150, 200, 0, 64, [0]),
     (40, 4, 4, 1, 2100, 33, 128, [33 - i % 34 for i in range(40)]),
+    # prefixes large enough to be read once for the batch
+    (8, 8, 8, 1, 1100, 20, 128, [20, 0, 3, 20, 19, 20, 1, 20]),
+    (2, 8, 4, 4, 9001, 30, 128, [30, 3]),
+    (17, 16, 1, 1, 7901, 40, 64, [i % 41 for i in range(5, 22)]),
+    (3, 6, 2, 21, 11003, 64, 128, [64, 20, 0]),
 ]
 
 
