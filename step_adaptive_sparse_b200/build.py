@@ -15,8 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libarea.so")
 SOURCES = ["api.cu", "pool_dwt.cu", "plan.cu", "attn_simt.cu", "attn_tc.cu", "noalloc.cu",
-           "bridge.cu", "schedule.cu", "cache_api.cu", "cache_simt.cu", "cache_dec.cu",
-           "cache_dec32.cu", "cache_tc.cu", "cache_join.cu", "evict.cu"]
+           "bridge.cu", "schedule.cu", "cache_api.cu", "cache_dec.cu", "cache_dec32.cu",
+           "cache_tc.cu", "cache_tc32.cu", "cache_join.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -27,12 +27,13 @@ def nvcc() -> str:
 
 # The window instantiations of attn_tc_kernel (template argument WINDOW =
 # true) split their registers with setmaxnreg: 128 threads at 136 and 256 at
-# 184, exactly the allocation of 384 threads at 168; cache_tc_kernel does the
-# same.  That holds only if ptxas gives them 168 registers at entry; the host
+# 184, exactly the allocation of 384 threads at 168; the cache kernels do
+# the same.  That holds only if ptxas gives them 168 registers at entry; the host
 # refuses the launch otherwise.  The build checks it here, and that no
 # tensor-core attention kernel spills.
 WINDOW_KERNEL_REGS = 168
-CHECKED = {"attn_tc.cu": "attn_tc_kernel", "cache_tc.cu": "cache_tc_kernel"}
+CHECKED = {"attn_tc.cu": "attn_tc_kernel", "cache_tc.cu": "cache_tc_kernel",
+           "cache_tc32.cu": "cache_tc32_kernel"}
 
 
 def check_attn_resources(ptxas_log: str, kernel: str = "attn_tc_kernel") -> list[str]:
@@ -56,7 +57,7 @@ def check_attn_resources(ptxas_log: str, kernel: str = "attn_tc_kernel") -> list
                 problems.append(f"{name}: {stores} bytes spill stores, {loads} bytes spill loads")
         elif "Used" in line and "registers" in line:
             regs = int(line.split("Used")[1].split()[0])
-            window = kernel == "cache_tc_kernel" or "attn_tc_kernelILb1E" in name
+            window = kernel != "attn_tc_kernel" or "attn_tc_kernelILb1E" in name
             if window and regs != WINDOW_KERNEL_REGS:
                 problems.append(f"{name}: {regs} registers at entry, the register split needs "
                                 f"{WINDOW_KERNEL_REGS}")

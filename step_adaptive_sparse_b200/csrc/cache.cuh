@@ -151,8 +151,8 @@ __host__ __device__ __forceinline__ KeyList key_list(const CacheArgs& a, const C
 // ---- host side ------------------------------------------------------------
 enum { CACHE_OP_SINK, CACHE_OP_PREFIX, CACHE_OP_WEIGHTS };
 
-// The kernels: for few rows, for many rows in fp32 and in bf16.
-enum { CACHE_DEC, CACHE_SIMT, CACHE_TC };
+// The kernels: for few rows, for many rows.
+enum { CACHE_DEC, CACHE_TC };
 // A launch of a call: the kernel, the rows and the splits of their keys.
 struct CacheLaunch {
   bool used;
@@ -172,8 +172,6 @@ struct CachePlan {
 int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int window, int sinks,
                int dtype, CachePlan* p);
 
-cudaError_t launch_cache_simt(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
-                              cudaStream_t s);
 cudaError_t launch_cache_dec_bf16(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
                                   cudaStream_t s);
 cudaError_t launch_cache_dec_f32(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
@@ -187,14 +185,17 @@ cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const flo
 cudaError_t launch_cache_weights(const CacheArgs& a, const float* logits, const float* lse,
                                  const float* acc, float* acco, cudaStream_t s);
 
-// Rows of a row tile of the tensor-core kernel: 128, or in a pooled launch as
+// Rows of a row tile of the bf16 tensor-core kernel: 128, or in a pooled launch as
 // many whole sequences' rows as fit.
 inline int tc_tile_rows(const CacheRows& rm) {
   return rm.pool_rows ? 128 / rm.pool_rows * rm.pool_rows : 128;
 }
 cudaError_t launch_cache_tc(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
                             cudaStream_t s);
+cudaError_t launch_cache_tc32(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
+                              cudaStream_t s);
 cudaError_t read_and_clear_cache_tc_error(int* code);
+cudaError_t read_and_clear_cache_tc32_error(int* code);
 
 struct EvictArgs {
   const void *k, *v;

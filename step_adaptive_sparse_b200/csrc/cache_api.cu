@@ -17,23 +17,22 @@ int64_t ceil256(int64_t n) { return (n + 255) & ~int64_t(255); }
 // Rows that one work item of a kernel takes.
 int rows_per_block(int kernel, int dtype, const CacheRows& rm) {
   switch (kernel) {
-    case CACHE_TC: return 2 * tc_tile_rows(rm);
-    case CACHE_SIMT: return 64;
+    case CACHE_TC: return dtype == AREA_DTYPE_BF16 ? 2 * tc_tile_rows(rm) : 128;
     default:
       if (dtype == AREA_DTYPE_BF16) return rm.RG <= 8 ? 8 : 16;
       return rm.RG <= 2 ? 2 : rm.RG <= 4 ? 4 : 8;
   }
 }
 
-// Splits of the tensor-core kernel's units: those that end first by a model of
-// its time.  A key tile takes a unit 1.8 us, starting and ending one 4 us, and
+// Splits of the tensor-core kernels' units: those that end first by a model of
+// their time.  128 keys take a unit `tile` us, starting and ending one 4 us, and
 // splits cost the join (5 us, and their outputs written and read again).
-int tc_splits(int64_t units, int64_t keys, int64_t rows, int D) {
+int tc_splits(int64_t units, int64_t keys, int64_t rows, int D, double tile) {
   const int64_t tiles = cdiv(keys, 128);
   int best = 1;
   double least = 0;
   for (int n = 1; n <= 64 && n <= cdiv(tiles, 2); ++n) {
-    const double t = cdiv(units * n, kSms) * (4.0 + 1.8 * (double)cdiv(tiles, n)) +
+    const double t = cdiv(units * n, kSms) * (4.0 + tile * (double)cdiv(tiles, n)) +
                      (n > 1 ? 5.0 + (double)rows * n * D * 8 / 5.0e6 : 0.0);
     if (n == 1 || t < least) {
       least = t;
@@ -51,12 +50,12 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D) {
   if (RG <= 16 || (op == CACHE_OP_WEIGHTS && dtype == AREA_DTYPE_BF16))
     l.kernel = CACHE_DEC;
   else
-    l.kernel = dtype == AREA_DTYPE_BF16 ? CACHE_TC : CACHE_SIMT;
+    l.kernel = CACHE_TC;
   const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, dtype, l.rows));
   int64_t n;
   if (l.kernel == CACHE_TC) {
-    n = tc_splits(blocks, keys, rows, D);
-  } else if (l.kernel == CACHE_DEC) {
+    n = tc_splits(blocks, keys, rows, D, dtype == AREA_DTYPE_BF16 ? 1.8 : D / 32.0);
+  } else {
     const int resident = (dtype == AREA_DTYPE_BF16 ? 3 : 2) * (int)kSms;
     if (blocks * 8 <= resident && (keys <= 4096 || blocks * 8 >= 2 * kSms)) {
       // All blocks run at once: a cluster of up to 8 joins its splits itself
@@ -72,9 +71,6 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D) {
       n = std::min(cdiv(32 * kSms, blocks), (keys + 512) / 1024);
       if (blocks * n < 2 * kSms) n = std::min(cdiv(2 * kSms, blocks), cdiv(keys, 128));
     }
-  } else {
-    // four blocks on each SM, at least two tiles of 64 keys to a split
-    n = std::min(cdiv(4 * kSms, blocks), cdiv(keys, 128));
   }
   l.nsplit = (int)std::max<int64_t>(n, 1);
 }
@@ -110,7 +106,7 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   CacheLaunch& m = p->main;
   m = CacheLaunch{};
   // one head's rows alone fill row tiles: heads need not share a tile
-  const bool per_head = Nq >= (dtype == AREA_DTYPE_BF16 ? 128 : 64);
+  const bool per_head = Nq >= 128;
   m.rows = CacheRows{per_head ? Nq : R, per_head ? B * H : B * Hk, per_head ? H / Hk : 1, 0,
                      P > 0 && !pool, S > 0};
   // keys that a block of up to 256 rows can see at most
@@ -177,8 +173,10 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     out.nsplit = l->nsplit;
     out.cluster = l->cluster;
     switch (l->kernel) {
-      case CACHE_TC: e = launch_cache_tc(a, l->rows, out, s); break;
-      case CACHE_SIMT: e = launch_cache_simt(a, l->rows, out, s); break;
+      case CACHE_TC:
+        e = dtype == AREA_DTYPE_BF16 ? launch_cache_tc(a, l->rows, out, s)
+                                     : launch_cache_tc32(a, l->rows, out, s);
+        break;
       default:
         e = dtype == AREA_DTYPE_BF16 ? launch_cache_dec_bf16(a, l->rows, out, s)
                                      : launch_cache_dec_f32(a, l->rows, out, s);

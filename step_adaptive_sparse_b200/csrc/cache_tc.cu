@@ -135,7 +135,7 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
           return false;
         if (lane == 0) {
           Unit u;
-          u.valid = decode_unit((int)(blockIdx.x + k * gridDim.x), prm, u) ? 1 : 0;
+          u.valid = decode_unit<128>((int)(blockIdx.x + k * gridDim.x), prm, u) ? 1 : 0;
           s_rec[slot] = u;
           mbar_arrive(bar(BAR_REC_FULL + slot));
         }
@@ -170,7 +170,7 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
             published = true;
             if (!(ok = publish(unit_count + 1))) break;
           }
-          const Tile t = tile_of(u, j);
+          const Tile t = tile_of<128>(u, j);
           for (int kv = 0; kv < 2; ++kv) {       // K then V
             const int s = (int)(kv_it % kStages);
             if (!warp_wait0(bar(BAR_KV_EMPTY + s), ((kv_it / kStages) & 1u) ^ 1u, abort_flag)) {
@@ -345,7 +345,7 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
       for (int j = first; j <= last;) {
         if (j - at32 >= 32) {
           at32 = j;
-          const Tile t = tile_of(u, min(j + lane, u.nt - 1));
+          const Tile t = tile_of<128>(u, min(j + lane, u.nt - 1));
           whole = __ballot_sync(0xffffffffu, t.n == 128 && (t.kind == 0 ? !prm.a.causal || whi > 0
                                                                         : whi >= t.j0 + 128 &&
                                              (wlo <= t.j0 || prm.a.sinks >= t.j0 + 128)));
@@ -358,7 +358,7 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
         tmem_ld128(tS, sr);
         if (masked) {
           // keys [ka, kb) and [0, kc) of the tile are this row's
-          const Tile t = tile_of(u, j);
+          const Tile t = tile_of<128>(u, j);
           const KeySpan sp = s_span[qt * 128 + trow];
           int ka = 0, kb, kc = 0;
           if (t.kind == 0) {
@@ -535,7 +535,7 @@ cudaError_t launch_cache_tc(const CacheArgs& a, const CacheRows& rm, const Cache
                             cudaStream_t s) {
   Maps m;
   cudaError_t e;
-  UnitParams p{a, rm, out, 0, tc_tile_rows(rm), 0, 0};
+  UnitParams p{a, rm, out, 0, tc_tile_rows(rm), 2, 0, 0};
   if (rm.pool_rows)
     e = make_map3(&m.q, a.q, a.B, (int64_t)a.Hk * rm.pool_rows, a.D, rm.pool_rows,
                   p.tile_rows / rm.pool_rows);

@@ -1,0 +1,507 @@
+// Attention over a key/value cache for many query rows (fp32) on the tensor
+// cores, without giving up fp32's precision.
+//
+// Every fp32 value is the exact sum of three bf16 values: its top 8 significand
+// bits, the next 8 and the last 8 (x = x0 + x1 + x2, cut off, not rounded, so
+// that no value overflows).  A product of two values is taken as the six terms
+//   x1 y1, x0 y2, x2 y0, x0 y1, x1 y0, x0 y0,
+// the small ones first; what is left out is below 2^-22 of it, and about 2^-25
+// on average.  That is six bf16 products for one of fp32, still four times
+// the rate of the CUDA cores (1643 / 6 against 64 TFLOP/s measured).
+// The accumulator of a chain of products loses up to a bit in each addition, so
+// a chain is kept short: one tile's scores, or one tile's 64 keys times their
+// values, whose sum is added in registers with the running output.
+//
+// A persistent CTA per SM of 384 threads: warps 0-3 read keys, values and
+// queries, cut them into their parts and write these as swizzled operand tiles
+// (rows past the list as zeros, so that nothing outside it is read); warp 4
+// issues the products; warps 8-11 do the softmax of one tile of 128 query rows
+// and hold its output, one row to a thread.  TMEM: S0 | S1 (64 columns each;
+// the weights' first two parts replace a tile's scores) | X0 | X1 (32 each, the
+// third part) | O0 | O1 (one tile's output, D each).  Products are issued as
+// QK(j + 1), PV(j), so that a tile's softmax runs under the other products; the
+// next keys are cut up while PV runs and the next values while QK does.
+// Work units and the keys of a row are as in the bf16 kernel, with one row tile
+// and key tiles of 64.  Every mbarrier wait is bounded.
+#include "cache_unit.cuh"
+#include "tc_common.cuh"
+
+namespace area {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kKT = 64;                    // keys of a tile
+constexpr int kRecSlots = 3;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// The other warpgroups get what the product warpgroup gives up; the sum is
+// exactly the allocation of a 168-register launch (checked before it).
+constexpr int kRegsRead = 200, kRegsMma = 56, kRegsSoft = 248;
+static_assert(kRegsRead + kRegsMma + kRegsSoft == 3 * 168, "register split");
+
+template <int D>
+struct Geo {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kQHalf = 128 * 128, kKHalf = kKT * 128;   // bytes of 64 columns
+  static constexpr int kQTerm = kHalves * kQHalf, kKTerm = kHalves * kKHalf;
+  static constexpr int kSmemK = 3 * kQTerm, kSmemV = kSmemK + 3 * kKTerm;
+  static constexpr int kSmemBar = kSmemV + 3 * kKTerm;
+  static constexpr int kSmemBytes = kSmemBar + 256 + 1024;       // barriers + alignment slack
+  static_assert(kSmemBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
+};
+
+enum {
+  BAR_Q_FULL = 0, BAR_Q_EMPTY, BAR_K_FULL, BAR_K_EMPTY, BAR_V_FULL, BAR_V_EMPTY,
+  BAR_S_FULL0, BAR_S_FULL1, BAR_P_FULL0, BAR_P_FULL1, BAR_O_FULL0, BAR_O_FULL1,
+  BAR_REC_FULL,
+  BAR_REC_EMPTY = BAR_REC_FULL + kRecSlots,
+  BAR_DRAIN = BAR_REC_EMPTY + kRecSlots,
+  BAR_COUNT
+};
+static_assert(BAR_COUNT * 8 <= 256, "barrier area");
+
+// The order of the six terms: parts of the first and of the second factor.
+__device__ __constant__ const int kPartA[6] = {1, 0, 2, 0, 1, 0};
+__device__ __constant__ const int kPartB[6] = {1, 2, 0, 1, 0, 0};
+
+// The top parts of two values, packed (a in the low half); what is left of the
+// values takes their place.
+__device__ __forceinline__ uint32_t cut2(float& a, float& b) {
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  a -= __uint_as_float(x & 0xffff0000u);
+  b -= __uint_as_float(y & 0xffff0000u);
+  return __byte_perm(x, y, 0x7632);
+}
+
+// The bits below n of a word.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t at, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3])
+               : "memory");
+}
+
+// Eight values of a row in registers, as the operand's 16-byte pieces: part t
+// at t * term.
+__device__ __forceinline__ void put8(uint32_t at, int term, float (&f)[8]) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = cut2(f[2 * i], f[2 * i + 1]);
+    st_shared16(at + t * term, w);
+  }
+}
+__device__ __forceinline__ void get8(const float* p, bool in, float (&f)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) x = __ldg(reinterpret_cast<const float4*>(p) + h);
+    f[4 * h] = x.x, f[4 * h + 1] = x.y, f[4 * h + 2] = x.z, f[4 * h + 3] = x.w;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
+  using G = Geo<D>;
+  constexpr int kChunks = D / 8;                  // 32-byte pieces of a row of fp32
+  constexpr int kPer = kKT * kChunks / 128;       // pieces of a thread and key tile
+  constexpr uint32_t kIdescS = idesc(kKT, false), kIdescO = idesc(D, true);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + G::kSmemBar;
+  __shared__ uint32_t s_tmem_base;
+  __shared__ int s_abort;
+  __shared__ __align__(16) Unit s_rec[kRecSlots];
+  __shared__ KeySpan s_span[128];          // of the softmax threads' rows
+  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    mbar_init(bar(BAR_Q_FULL), 128);
+    mbar_init(bar(BAR_Q_EMPTY), 1);
+    mbar_init(bar(BAR_K_FULL), 128);
+    mbar_init(bar(BAR_K_EMPTY), 1);
+    mbar_init(bar(BAR_V_FULL), 128);
+    mbar_init(bar(BAR_V_EMPTY), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(BAR_S_FULL0 + t), 1);
+      mbar_init(bar(BAR_P_FULL0 + t), 128);
+      mbar_init(bar(BAR_O_FULL0 + t), 1);
+    }
+    for (int s = 0; s < kRecSlots; ++s) {
+      mbar_init(bar(BAR_REC_FULL + s), 1);
+      mbar_init(bar(BAR_REC_EMPTY + s), 8);   // warps 1-3, the MMA thread, 4 softmax warps
+    }
+    mbar_init(bar(BAR_DRAIN), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&s_tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem_base;
+  constexpr uint32_t kColX = 128, kColO = 192;
+  int* abort_flag = &s_abort;
+
+  // the paths must not meet again before the end (see the bf16 kernel)
+  if (warp < 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRead) : "memory");
+    // ---------------------------------------------- reading and cutting up
+    const int tid = threadIdx.x, ch = tid % kChunks, row0 = tid / kChunks;
+    constexpr int kRowStep = 128 / kChunks;
+    uint32_t k_it = 0, v_it = 0, unit_count = 0;
+    bool ok = true;
+    auto publish = [&](uint32_t k) -> bool {
+      const uint32_t slot = k % kRecSlots;
+      if (!warp_wait0(bar(BAR_REC_EMPTY + slot), ((k / kRecSlots) & 1u) ^ 1u, abort_flag))
+        return false;
+      if (lane == 0) {
+        Unit u;
+        u.valid = decode_unit<kKT>((int)(blockIdx.x + k * gridDim.x), prm, u) ? 1 : 0;
+        s_rec[slot] = u;
+        mbar_arrive(bar(BAR_REC_FULL + slot));
+      }
+      __syncwarp();
+      return true;
+    };
+    if (warp == 0) ok = publish(0);
+    while (ok) {
+      const uint32_t slot = unit_count % kRecSlots;
+      if (!(ok = warp_wait_all(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u,
+                               abort_flag)))
+        break;
+      const Unit& u = s_rec[slot];
+      if (!u.valid) break;
+      if (warp == 0 && !(ok = publish(unit_count + 1))) break;
+      const int nt = u.nt;
+      float kf[kPer][8], vf[kPer][8];
+      auto load = [&](float (&f)[kPer][8], int j, bool val) {
+        const Tile t = tile_of<kKT>(u, j);
+        const float* base = static_cast<const float*>(t.kind ? (val ? prm.a.v : prm.a.k)
+                                                             : (val ? prm.a.vp : prm.a.kp)) +
+                            ((int64_t)(t.kind ? u.kvh : u.ph) * (t.kind ? prm.a.S : prm.a.P) +
+                             t.j0) * D + ch * 8;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int r = row0 + i * kRowStep;
+          get8(base + (int64_t)r * D, r < t.n, f[i]);
+        }
+      };
+      auto put = [&](float (&f)[kPer][8], int at) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int r = row0 + i * kRowStep;
+          put8(sbase + at + (ch >> 3) * G::kKHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+               G::kKTerm, f[i]);
+        }
+        fence_proxy_async();
+      };
+      if (nt > 0) load(kf, 0, false);
+      // queries
+      if (!(ok = warp_wait_all(bar(BAR_Q_EMPTY), (unit_count & 1u) ^ 1u, abort_flag))) break;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kChunks; i0 += kPer) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int rr = u.r0[0] + row0 + (i0 + i) * kRowStep;
+          const bool in = rr < prm.rm.RG;
+          const int64_t row = in ? cache_row(prm.a, prm.rm, u.g, rr).row : 0;
+          get8(static_cast<const float*>(prm.a.q) + row * D + ch * 8, in, vf[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int r = row0 + (i0 + i) * kRowStep;
+          put8(sbase + (ch >> 3) * G::kQHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), G::kQTerm,
+               vf[i]);
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive(bar(BAR_Q_FULL));
+      // K(j + 1) before V(j): the order in which their buffers become free
+      for (int j = -1; j < nt; ++j) {
+        if (j + 1 < nt) {
+          if (!(ok = warp_wait_all(bar(BAR_K_EMPTY), (k_it & 1u) ^ 1u, abort_flag))) break;
+          put(kf, G::kSmemK);
+          mbar_arrive(bar(BAR_K_FULL));
+          ++k_it;
+          if (j + 2 < nt) load(kf, j + 2, false);
+        }
+        if (j >= 0) {
+          if (!(ok = warp_wait_all(bar(BAR_V_EMPTY), (v_it & 1u) ^ 1u, abort_flag))) break;
+          put(vf, G::kSmemV);
+          mbar_arrive(bar(BAR_V_FULL));
+          ++v_it;
+        }
+        if (j + 1 < nt) load(vf, j + 1, true);
+      }
+      if (!ok) break;
+      if (warp != 0 && lane == 0) mbar_arrive(bar(BAR_REC_EMPTY + slot));
+      ++unit_count;
+    }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma) : "memory");
+    // -------------------------------------------------------------- products
+    if (warp == 4 && lane == 0) {
+      uint32_t unit_count = 0;
+      uint32_t s_it = 0, p_it = 0;     // tiles whose scores, whose outputs have been issued
+      bool ok = true;
+      auto qk = [&]() -> bool {
+        if (!mbar_wait(bar(BAR_K_FULL), s_it & 1u, abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + (s_it & 1u) * 64;
+#pragma unroll 1
+        for (int t = 0; t < 6; ++t) {
+          const uint32_t qs = sbase + kPartA[t] * G::kQTerm;
+          const uint32_t ks = sbase + G::kSmemK + kPartB[t] * G::kKTerm;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(d, sdesc(qs + (kk >> 2) * G::kQHalf + (kk & 3) * 32, 16, 1024),
+                   sdesc(ks + (kk >> 2) * G::kKHalf + (kk & 3) * 32, 16, 1024), kIdescS,
+                   (t > 0 || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(bar(BAR_S_FULL0 + (s_it & 1u)));
+        mma_commit(bar(BAR_K_EMPTY));
+        ++s_it;
+        return true;
+      };
+      auto pv = [&]() -> bool {
+        const uint32_t b = p_it & 1u, ph = (p_it >> 1) & 1u;
+        if (!mbar_wait(bar(BAR_V_FULL), p_it & 1u, abort_flag)) return false;
+        if (!mbar_wait(bar(BAR_P_FULL0 + b), ph, abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + kColO + b * D;
+#pragma unroll 1
+        for (int t = 0; t < 6; ++t) {
+          const int pa = kPartA[t];
+          const uint32_t p = tmem + (pa < 2 ? b * 64 + pa * 32 : kColX + b * 32);
+          const uint32_t vs = sbase + G::kSmemV + kPartB[t] * G::kKTerm;
+#pragma unroll
+          for (int kk = 0; kk < kKT / 16; ++kk)
+            mma_ts(d, p + kk * 8, sdesc(vs + kk * 2048, G::kKHalf, 1024), kIdescO,
+                   (t > 0 || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(bar(BAR_O_FULL0 + b));
+        mma_commit(bar(BAR_V_EMPTY));
+        ++p_it;
+        return true;
+      };
+      while (ok) {
+        const uint32_t slot = unit_count % kRecSlots;
+        if (!(ok = mbar_wait(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u, abort_flag)))
+          break;
+        const int valid = s_rec[slot].valid, nt = s_rec[slot].nt;
+        mbar_arrive(bar(BAR_REC_EMPTY + slot));
+        if (!valid) break;
+        if (!(ok = mbar_wait(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
+        if (nt == 0) mma_commit(bar(BAR_Q_EMPTY));
+        for (int j = 0; j < nt; ++j) {
+          if (j == 0 && !(ok = qk())) break;
+          if (j + 1 < nt && !(ok = qk())) break;
+          if (j == (nt > 1 ? nt - 2 : 0))
+            mma_commit(bar(BAR_Q_EMPTY));              // the unit's scores are all issued
+          if (!(ok = pv())) break;
+        }
+        if (!ok) break;
+        ++unit_count;
+      }
+      int drain_abort = 0;
+      mma_commit(bar(BAR_DRAIN));
+      mbar_wait(bar(BAR_DRAIN), 0, &drain_abort);
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft) : "memory");
+    // ------------------------------------------------------ softmax / output
+    const int trow = ((warp & 3) << 5) + lane;       // TMEM lane = row of the tile
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) << 5) << 16);
+    uint32_t it = 0, unit_count = 0;                 // tiles so far, over all units
+    const float sl2 = prm.a.scale_log2;
+    bool ok = true;
+    while (ok) {
+      const uint32_t slot = unit_count % kRecSlots;
+      if (!(ok = warp_wait_all(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u,
+                               abort_flag)))
+        break;
+      const Unit& u = s_rec[slot];
+      if (!u.valid) break;
+      // this thread's row and what it sees; rows that do not exist see all
+      const int r = u.r0[0] + trow;
+      const bool rvalid = r < prm.rm.RG;
+      // (kept in shared memory: the output and a score row fill the registers)
+      {
+        KeySpan sp{0, INT_MAX};
+        if (rvalid) {
+          const CacheRow cr = cache_row(prm.a, prm.rm, u.g, r);
+          sp = key_span(prm.a, cache_len(prm.a, cr.b), cr.i);
+        }
+        s_span[trow] = sp;
+      }
+      const int nt = u.nt;
+      float m = -INFINITY, l = 0.f, o[D];
+#pragma unroll
+      for (int i = 0; i < D; ++i) o[i] = 0.f;
+      // adds tile k's output
+      auto add_output = [&](uint32_t k) -> bool {
+        if (!warp_wait_all(bar(BAR_O_FULL0 + (k & 1u)), (k >> 1) & 1u, abort_flag)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t t[32];
+          tmem_ld32(tl + kColO + (k & 1u) * D + c * 32, t);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[c * 32 + i] += __uint_as_float(t[i]);
+        }
+        tc_fence_before();
+        return true;
+      };
+      for (int j = 0; j < nt; ++j, ++it) {
+        const Tile t = tile_of<kKT>(u, j);
+        // the tile's keys that this row sees, one bit each
+        uint32_t sees0, sees1;
+        {
+          const KeySpan sp = s_span[trow];
+          int ka = 0, kb, kc = 0;
+          if (t.kind == 0) {
+            kb = sees_prefix(prm.a, sp) ? t.n : 0;
+          } else {
+            ka = sp.lo - t.j0;
+            kb = min(sp.hi - t.j0, t.n);
+            kc = min(prm.a.sinks - t.j0, kb);
+          }
+          sees0 = (bits_below(kb) & ~bits_below(ka)) | bits_below(kc);
+          sees1 = (bits_below(kb - 32) & ~bits_below(ka - 32)) | bits_below(kc - 32);
+        }
+        if (!(ok = warp_wait_all(bar(BAR_S_FULL0 + (it & 1u)), (it >> 1) & 1u, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t tS = tl + (it & 1u) * 64, tX = tl + kColX + (it & 1u) * 32;
+        float s[kKT];
+        tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+        tmem_ld32(tS + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
+        if (prm.out.logits && rvalid) {
+          // (scores are asked for in launches that are not pooled)
+          float* dst = prm.out.logits + ((int64_t)u.g * prm.rm.RG + r) * prm.a.S + t.j0;
+#pragma unroll
+          for (int i = 0; i < kKT; ++i)
+            if (i < t.n) dst[i] = s[i] * sl2;
+        }
+        if (__any_sync(0xffffffffu, (sees0 & sees1) != 0xffffffffu)) {
+#pragma unroll
+          for (int i = 0; i < kKT; ++i)
+            if (!((i < 32 ? sees0 : sees1) >> (i & 31) & 1u)) s[i] = -INFINITY;   // no weight
+        }
+        float pm[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < kKT; i += 2) pm[(i >> 1) & 3] = max3(pm[(i >> 1) & 3], s[i], s[i + 1]);
+        const float mnew = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl2, m);
+        const bool rescale = __any_sync(0xffffffffu, mnew > m + kRescaleThreshold);
+        const float alpha = rescale ? (m == -INFINITY ? 0.f : fast_exp2(m - mnew)) : 1.f;
+        if (rescale) m = mnew;
+        l *= alpha;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const float negm = m == -INFINITY ? 0.f : -m;     // nothing seen so far: all weights 0
+#pragma unroll
+        for (int i = 0; i < kKT; i += 2) {
+          float x0, x1;
+          fma2(x0, x1, s[i], s[i + 1], sl2, negm);
+          s[i] = fast_exp2(x0);
+          s[i + 1] = fast_exp2(x1);
+          if ((i >> 1) & 1) add2(ls[2], ls[3], s[i], s[i + 1]); else add2(ls[0], ls[1], s[i], s[i + 1]);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        // the weights' parts, one after the other: what is left takes their place
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) p[i] = cut2(s[2 * i], s[2 * i + 1]);
+          tmem_st32(part < 2 ? tS + part * 32 : tX, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(BAR_P_FULL0 + (it & 1u)));
+        if (j > 0 && !(ok = add_output(it - 1))) break;
+        if (rescale) {
+#pragma unroll
+          for (int i = 0; i < D; ++i) o[i] *= alpha;
+        }
+      }
+      if (!ok) break;
+      if (nt > 0 && !(ok = add_output(it - 1))) break;
+      // ---- epilogue
+      if (rvalid) {
+        const int64_t row = cache_row(prm.a, prm.rm, u.g, r).row;
+        const int64_t at = (int64_t)(prm.out.slot0 + u.sp) * prm.out.rows + row;
+        if (!prm.out.direct) prm.out.part_ml[at] = make_float2(m, l);
+        const float mul = !prm.out.direct ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        float* dst = prm.out.direct ? static_cast<float*>(prm.a.o) + row * D
+                                    : prm.out.part_o + at * D;
+        if (prm.out.direct || l != 0.f) {
+#pragma unroll
+          for (int c = 0; c < D; c += 8) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = o[c + i] * mul;
+            st_global_v8f(dst + c, f);
+          }
+        }
+      }
+      if (lane == 0) mbar_arrive(bar(BAR_REC_EMPTY + slot));
+      ++unit_count;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int D>
+cudaError_t launch(const UnitParams& prm, cudaStream_t s) {
+  auto fn = cache_tc32_kernel<D>;
+  constexpr int kSmem = Geo<D>::kSmemBytes;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, fn);
+  if (e != cudaSuccess) return e;
+  // setmaxnreg.inc waits until the registers it asks for are free, so the split
+  // must fit in what the launch allocates
+  if (fa.numRegs != 168) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  fn<<<std::min(prm.units, num_sms()), kThreads, kSmem, s>>>(prm);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t read_and_clear_cache_tc32_error(int* code) {
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyFromSymbol(code, g_tc_error, sizeof(int));
+  if (e != cudaSuccess) return e;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(g_tc_error, &zero, sizeof(int));
+}
+
+cudaError_t launch_cache_tc32(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
+                              cudaStream_t s) {
+  UnitParams p{a, rm, out, (rm.RG + 127) / 128, 128, 1, 0, 0};
+  p.units = (int)((int64_t)rm.groups * p.nrb * out.nsplit);
+  p.heavy_first = a.causal && !rm.pool_rows && a.window >= a.S;
+  return a.D == 64 ? launch<64>(p, s) : launch<128>(p, s);
+}
+
+}  // namespace area

@@ -1,6 +1,7 @@
-// How the tensor-core kernel of cache_tc.cu cuts a launch into work units: two
-// row tiles of a group and a split of the list of keys that they see.  Integer
-// arithmetic alone, also compiled for the host and checked there.
+// How the tensor-core kernels cut a launch into work units: two row tiles of a
+// group (fp32: one) and a split of the list of keys that they see, in tiles of
+// KT keys.  Integer arithmetic alone, also compiled for the host and checked
+// there.
 #pragma once
 
 #include "cache.cuh"
@@ -26,8 +27,9 @@ struct UnitParams {
   CacheArgs a;
   CacheRows rm;
   CacheOut out;
-  int nrb;                 // pairs of row tiles of a group
-  int tile_rows;           // rows of a row tile: 128, pooled: whole sequences
+  int nrb;                 // units that a group's rows make
+  int tile_rows;           // rows of a row tile
+  int tiles;               // row tiles of a unit
   int units;
   int heavy_first;         // row tiles from the last to the first, over all groups
 };
@@ -38,26 +40,27 @@ struct Tile {
   int j0, n;               // first key, keys
   bool copy;               // copied row by row
 };
+template <int KT>
 __host__ __device__ __forceinline__ Tile tile_of(const Unit& u, int j) {
   Tile t;
   int i = u.t0 + j;
   if (i < u.tp) {
     t.kind = 0;
-    t.j0 = i * 128;
-    t.n = min(128, u.kl.np - t.j0);
+    t.j0 = i * KT;
+    t.n = min(KT, u.kl.np - t.j0);
     t.copy = false;                        // its map ends with the prefix
     return t;
   }
   i -= u.tp;
   t.kind = 1;
   if (i < u.ts) {
-    t.j0 = i * 128;
-    t.n = min(128, u.kl.ns - t.j0);
+    t.j0 = i * KT;
+    t.n = min(KT, u.kl.ns - t.j0);
   } else {
-    t.j0 = u.kl.lo + (i - u.ts) * 128;
-    t.n = min(128, u.hi - t.j0);
+    t.j0 = u.kl.lo + (i - u.ts) * KT;
+    t.n = min(KT, u.hi - t.j0);
   }
-  t.copy = t.n < 128 && !(t.j0 >= u.safe_lo && t.j0 + 128 <= u.safe_hi);
+  t.copy = t.n < KT && !(t.j0 >= u.safe_lo && t.j0 + KT <= u.safe_hi);
   return t;
 }
 __host__ __device__ __forceinline__ bool is_active(const Unit& u, int t, int j) {
@@ -88,6 +91,7 @@ __host__ __device__ __forceinline__ TileRange tile_range(const Unit& u, int t) {
 }
 
 // Unit idx of a launch; false behind the last one.
+template <int KT>
 __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& u) {
   const CacheArgs& a = p.a;
   const CacheRows& rm = p.rm;
@@ -102,17 +106,17 @@ __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& 
     rb = rest % p.nrb;
     u.g = rest / p.nrb;
   }
-  u.r0[0] = rb * 2 * p.tile_rows;
+  u.r0[0] = rb * p.tiles * p.tile_rows;
   u.r0[1] = min(u.r0[0] + p.tile_rows, rm.RG);
-  const int r1 = min(u.r0[0] + 2 * p.tile_rows, rm.RG);
+  const int r1 = min(u.r0[0] + p.tiles * p.tile_rows, rm.RG);
   u.kvh = rm.pool_rows ? 0 : u.g / rm.kv_div;
   u.ph = rm.pool_rows ? u.g : u.kvh % a.Hk;
   const int b = rm.pool_rows ? 0 : u.kvh / a.Hk;
   u.kl = key_list(a, rm, b, u.r0[0], r1);
   u.hi = u.kl.lo + (u.kl.total - u.kl.np - u.kl.ns);
-  u.tp = (u.kl.np + 127) / 128;
-  u.ts = (u.kl.ns + 127) / 128;
-  const int to = (u.hi - u.kl.lo + 127) / 128;
+  u.tp = (u.kl.np + KT - 1) / KT;
+  u.ts = (u.kl.ns + KT - 1) / KT;
+  const int to = (u.hi - u.kl.lo + KT - 1) / KT;
   const int ntile = u.tp + u.ts + to;
   u.t0 = (int)((int64_t)ntile * u.sp / p.out.nsplit);
   const int t1 = (int)((int64_t)ntile * (u.sp + 1) / p.out.nsplit);
@@ -141,8 +145,8 @@ __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& 
     }
     if (a.sinks > u.kl.lo) lo = u.kl.lo;         // sinks among the first own tiles
     const int base = u.tp + u.ts - u.t0;         // the first own tile, in this split's count
-    u.oa[t] = max(0, min(u.nt, base + (lo - u.kl.lo) / 128));
-    u.ob[t] = max(u.oa[t], min(u.nt, base + (hi - u.kl.lo + 127) / 128));
+    u.oa[t] = max(0, min(u.nt, base + (lo - u.kl.lo) / KT));
+    u.ob[t] = max(u.oa[t], min(u.nt, base + (hi - u.kl.lo + KT - 1) / KT));
   }
   return true;
 }

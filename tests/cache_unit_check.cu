@@ -13,10 +13,12 @@
 
 using namespace area;
 
+template <int KT, int TILES>
 static int check(const CacheArgs& a, const CacheRows& rm, int nsplit) {
-  UnitParams p{a, rm, CacheOut{}, 0, tc_tile_rows(rm), 0, 0};
+  UnitParams p{a, rm, CacheOut{}, 0, TILES == 2 ? tc_tile_rows(rm) : 128, TILES, 0, 0};
   p.out.nsplit = nsplit;
-  p.nrb = (rm.RG + 2 * p.tile_rows - 1) / (2 * p.tile_rows);
+  const int unit_rows = TILES * p.tile_rows;
+  p.nrb = (rm.RG + unit_rows - 1) / unit_rows;
   p.units = rm.groups * p.nrb * nsplit;
   for (int heavy = 0; heavy < 2; ++heavy) {
     p.heavy_first = heavy;
@@ -25,19 +27,19 @@ static int check(const CacheArgs& a, const CacheRows& rm, int nsplit) {
     std::vector<unsigned char> met((size_t)rows * keys, 0), touched(rows, 0);
     Unit u;
     for (int idx = 0; idx < p.units; ++idx) {
-      if (!decode_unit(idx, p, u)) return printf("unit %d missing\n", idx), 1;
+      if (!decode_unit<KT>(idx, p, u)) return printf("unit %d missing\n", idx), 1;
       for (int j = 0; j < u.nt; ++j) {
-        const Tile t = tile_of(u, j);
-        if (t.n < 1 || t.n > 128 || t.j0 < 0) return printf("tile of %d keys at %d\n", t.n, t.j0), 1;
+        const Tile t = tile_of<KT>(u, j);
+        if (t.n < 1 || t.n > KT || t.j0 < 0) return printf("tile of %d keys at %d\n", t.n, t.j0), 1;
         if (t.j0 + t.n > (t.kind ? a.S : a.P)) return printf("tile past its tensor\n"), 1;
         if (t.kind && !t.copy) {
           const int b = u.kvh / a.Hk, len = cache_len(a, b);
           const int lo = key_span(a, len, 0).lo;
-          for (int key = t.j0; key < std::min(t.j0 + 128, a.S); ++key)
+          for (int key = t.j0; key < std::min(t.j0 + KT, a.S); ++key)
             if (key >= len || (key < lo && key >= a.sinks)) return printf("row %d loaded\n", key), 1;
         }
       }
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < TILES; ++t) {
         const int first = first_tile(u, t), last = last_tile(u, t);
         int n = 0;
         for (int j = 0; j < u.nt; ++j) {
@@ -60,7 +62,7 @@ static int check(const CacheArgs& a, const CacheRows& rm, int nsplit) {
           const KeySpan sp = key_span(a, cache_len(a, cr.b), cr.i);
           for (int j = 0; j < u.nt; ++j) {
             if (!is_active(u, t, j)) continue;
-            const Tile tl = tile_of(u, j);
+            const Tile tl = tile_of<KT>(u, j);
             for (int x = 0; x < tl.n; ++x) {
               const int key = tl.j0 + x;
               // the limits that the kernel applies to a row's scores
@@ -72,7 +74,7 @@ static int check(const CacheArgs& a, const CacheRows& rm, int nsplit) {
         }
       }
     }
-    if (decode_unit(p.units, p, u)) return printf("a unit too many\n"), 1;
+    if (decode_unit<KT>(p.units, p, u)) return printf("a unit too many\n"), 1;
     for (int row = 0; row < rows; ++row) {
       if (touched[row] != nsplit) return printf("row %d in %d splits\n", row, touched[row]), 1;
       const int b = row / (a.H * a.Nq), i = row % a.Nq, len = cache_len(a, b);
@@ -120,13 +122,13 @@ int main() {
     const int nsplit = 1 + (rnd(2) ? rnd(6) : 0);
     const CacheRows own{per_head ? Nq : R, per_head ? B * G * Hk : B * Hk, per_head ? G : 1, 0,
                         a.P > 0, 1};
-    if (check(a, own, nsplit))
+    if (check<128, 2>(a, own, nsplit) || check<64, 1>(a, own, nsplit))
       return printf("B=%d Hk=%d G=%d Nq=%d P=%d S=%d window=%d sinks=%d per_head=%d\n", B, Hk, G, Nq,
                     a.P, S, a.window, a.sinks, per_head), 1;
     ++cases;
     if (a.P > 0 && R < 64) {
       const CacheRows pooled{B * R, Hk, 1, R, 1, 0};
-      if (check(a, pooled, nsplit)) return printf("pooled B=%d R=%d P=%d\n", B, R, a.P), 1;
+      if (check<128, 2>(a, pooled, nsplit) || check<64, 1>(a, pooled, nsplit)) return printf("pooled B=%d R=%d P=%d\n", B, R, a.P), 1;
       ++cases;
     }
   }
