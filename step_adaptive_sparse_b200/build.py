@@ -16,7 +16,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libarea.so")
 SOURCES = ["api.cu", "pool_dwt.cu", "plan.cu", "attn_simt.cu", "attn_tc.cu", "noalloc.cu",
            "bridge.cu", "schedule.cu", "cache_api.cu", "cache_dec.cu", "cache_dec32.cu",
-           "cache_tc.cu", "cache_tc32.cu", "cache_join.cu", "evict.cu"]
+           "cache_tc.cu", "cache_tc32.cu", "cache_weights.cu", "cache_join.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

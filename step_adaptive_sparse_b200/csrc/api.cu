@@ -117,6 +117,9 @@ int area_kernel_error(int* code) {
   st = finish(area::read_and_clear_cache_tc32_error(&ca));
   if (st != AREA_OK) return st;
   tc |= ca;
+  st = finish(area::read_and_clear_cache_weights_error(&ca));
+  if (st != AREA_OK) return st;
+  tc |= ca;
   *code = tc | (pl ? AREA_KERR_PLAN_BARRIER : 0);
   return AREA_OK;
 }

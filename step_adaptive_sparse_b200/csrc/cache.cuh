@@ -53,7 +53,9 @@ struct CacheOut {
   int direct;        // 1: one split in all, the output is written to o
   float* part_o;     // [slots][rows][D]
   float2* part_ml;   // [slots][rows] (m, l)
-  float* logits;     // [rows][S] scores in log2 units, or null
+  float* logits;     // [rows][S] scores in log2 units, or null (kernels for few rows)
+  float* lse;        // [rows] log2-sums, +inf without a key, or null (kernels for many
+                     // rows, when direct)
   int64_t rows;      // B * H * Nq
   const float* acc;  // with a direct launch that has scores: the weights' sums
   float* acco;
@@ -196,6 +198,11 @@ cudaError_t launch_cache_tc32(const CacheArgs& a, const CacheRows& rm, const Cac
                               cudaStream_t s);
 cudaError_t read_and_clear_cache_tc_error(int* code);
 cudaError_t read_and_clear_cache_tc32_error(int* code);
+// The same sums as launch_cache_weights for many rows of a key head: the scores
+// are computed once more instead of read.
+cudaError_t launch_cache_weights_tc(const CacheArgs& a, const float* lse, const float* acc,
+                                    float* acco, int dtype, cudaStream_t s);
+cudaError_t read_and_clear_cache_weights_error(int* code);
 
 struct EvictArgs {
   const void *k, *v;

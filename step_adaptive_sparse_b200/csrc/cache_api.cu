@@ -47,10 +47,7 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D) {
   const int RG = l.rows.RG;
   l.used = true;
   l.cluster = 1;
-  if (RG <= 16 || (op == CACHE_OP_WEIGHTS && dtype == AREA_DTYPE_BF16))
-    l.kernel = CACHE_DEC;
-  else
-    l.kernel = CACHE_TC;
+  l.kernel = RG <= 16 ? CACHE_DEC : CACHE_TC;
   const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, dtype, l.rows));
   int64_t n;
   if (l.kernel == CACHE_TC) {
@@ -119,17 +116,18 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
     cut(p->pooled, op, dtype, P, p->rows, D);
     p->slots += p->pooled.nsplit / p->pooled.cluster;
   }
-  // The scores' softmax needs the whole row's sum: the kernel for few rows has
-  // it when one block or cluster has all of a key head's rows and splits.
-  const bool whole = op != CACHE_OP_WEIGHTS ||
-                     (m.kernel == CACHE_DEC &&
-                      m.rows.RG <= rows_per_block(CACHE_DEC, dtype, m.rows) && m.rows.kv_div == 1);
+  // The weights need a row's whole sum: the kernel for few rows has it when one
+  // block or cluster has all of a key head's rows and splits, and adds them up
+  // from its scores; the others leave the sums for a launch of its own.
+  const bool weights = op == CACHE_OP_WEIGHTS, few = m.kernel == CACHE_DEC;
+  const bool whole = !weights || !few || m.rows.RG <= rows_per_block(CACHE_DEC, dtype, m.rows);
   if (p->slots == 1 && whole) p->slots = 0;
   p->off_ml = 0;
   p->off_o = p->off_ml + ceil256(p->slots * p->rows * 8);
   p->off_lse = p->off_o + ceil256(p->slots * p->rows * D * 4);
-  p->off_logits = p->off_lse + (op == CACHE_OP_WEIGHTS && p->slots ? ceil256(p->rows * 4) : 0);
-  p->bytes = p->off_logits + (op == CACHE_OP_WEIGHTS ? ceil256(p->rows * S * 4) : 0);
+  p->off_logits = p->off_lse + (weights && (p->slots || !few) ? ceil256(p->rows * 4) : 0);
+  if (p->rows > (int64_t(1) << 58) / (S + 1)) return AREA_EUNSUPPORTED;
+  p->bytes = p->off_logits + (weights && few ? ceil256(p->rows * S * 4) : 0);
   const int64_t blocks = cdiv(m.rows.RG, 8) * m.rows.groups * std::max(m.nsplit, 1);
   if (blocks > INT_MAX || cdiv(S, 256) * B * Hk > INT_MAX) return AREA_EUNSUPPORTED;
   return AREA_OK;
@@ -161,10 +159,14 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     out.part_ml = reinterpret_cast<float2*>(w + p.off_ml);
     out.part_o = reinterpret_cast<float*>(w + p.off_o);
   }
-  if (op == CACHE_OP_WEIGHTS) {
+  const bool weights = op == CACHE_OP_WEIGHTS, few = p.main.kernel == CACHE_DEC;
+  float* lse = weights && (p.slots || !few) ? reinterpret_cast<float*>(w + p.off_lse) : nullptr;
+  if (weights && few) {
     out.logits = reinterpret_cast<float*>(w + p.off_logits);
     out.acc = acc;
     out.acco = acco;
+  } else if (out.direct) {
+    out.lse = lse;
   }
   cudaError_t e;
   const CacheLaunch* ls[2] = {&p.main, &p.pooled};
@@ -184,11 +186,13 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     if (e != cudaSuccess) return fail_cuda(e);
     out.slot0 += l->nsplit / l->cluster;
   }
-  if (!p.slots) return AREA_OK;
-  float* lse = op == CACHE_OP_WEIGHTS ? reinterpret_cast<float*>(w + p.off_lse) : nullptr;
-  e = launch_cache_join(a, out.part_o, out.part_ml, p.slots, p.rows, lse, dtype, s);
-  if (e != cudaSuccess || op != CACHE_OP_WEIGHTS) return finish(e);
-  return finish(launch_cache_weights(a, out.logits, lse, acc, acco, s));
+  if (p.slots) {
+    e = launch_cache_join(a, out.part_o, out.part_ml, p.slots, p.rows, lse, dtype, s);
+    if (e != cudaSuccess) return fail_cuda(e);
+  }
+  if (!lse) return AREA_OK;
+  return finish(few ? launch_cache_weights(a, out.logits, lse, acc, acco, s)
+                    : launch_cache_weights_tc(a, lse, acc, acco, dtype, s));
 }
 
 int ws_bytes_of(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int window, int sinks,

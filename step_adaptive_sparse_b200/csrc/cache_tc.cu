@@ -441,6 +441,7 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
         tc_fence_after();
       }
       if (!prm.out.direct && rvalid) prm.out.part_ml[at] = make_float2(m, l);
+      if (prm.out.lse && rvalid) prm.out.lse[row] = l == 0.f ? INFINITY : m + log2f(l);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (prm.out.direct || last >= 0) {
 #pragma unroll 1
@@ -484,22 +485,6 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-}
-
-// bf16 map over [n2, n1, D] (rows of n1 at D values, planes n2 at `plane`
-// rows) with a box of 64 columns x b1 x b2.  Rows past n1 read as zeros.
-cudaError_t make_map3(CUtensorMap* m, const void* base, int64_t n2, int64_t n1, int D, int b1,
-                      int b2) {
-  auto enc = get_encode();
-  if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)n1, (cuuint64_t)n2};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)n1 * D * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int D>

@@ -24,6 +24,7 @@
 // Work units and the keys of a row are as in the bf16 kernel, with one row tile
 // and key tiles of 64.  Every mbarrier wait is bounded.
 #include "cache_unit.cuh"
+#include "cut3.cuh"
 #include "tc_common.cuh"
 
 namespace area {
@@ -35,7 +36,7 @@ constexpr int kRecSlots = 3;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // The other warpgroups get what the product warpgroup gives up; the sum is
 // exactly the allocation of a 168-register launch (checked before it).
-constexpr int kRegsRead = 200, kRegsMma = 56, kRegsSoft = 248;
+constexpr int kRegsRead = 192, kRegsMma = 56, kRegsSoft = 256;
 static_assert(kRegsRead + kRegsMma + kRegsSoft == 3 * 168, "register split");
 
 template <int D>
@@ -59,48 +60,9 @@ enum {
 };
 static_assert(BAR_COUNT * 8 <= 256, "barrier area");
 
-// The order of the six terms: parts of the first and of the second factor.
-__device__ __constant__ const int kPartA[6] = {1, 0, 2, 0, 1, 0};
-__device__ __constant__ const int kPartB[6] = {1, 2, 0, 1, 0, 0};
-
-// The top parts of two values, packed (a in the low half); what is left of the
-// values takes their place.
-__device__ __forceinline__ uint32_t cut2(float& a, float& b) {
-  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
-  a -= __uint_as_float(x & 0xffff0000u);
-  b -= __uint_as_float(y & 0xffff0000u);
-  return __byte_perm(x, y, 0x7632);
-}
-
 // The bits below n of a word.
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
-__device__ __forceinline__ void st_shared16(uint32_t at, const uint32_t (&w)[4]) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
-               "r"(w[2]), "r"(w[3])
-               : "memory");
-}
-
-// Eight values of a row in registers, as the operand's 16-byte pieces: part t
-// at t * term.
-__device__ __forceinline__ void put8(uint32_t at, int term, float (&f)[8]) {
-#pragma unroll
-  for (int t = 0; t < 3; ++t) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = cut2(f[2 * i], f[2 * i + 1]);
-    st_shared16(at + t * term, w);
-  }
-}
-__device__ __forceinline__ void get8(const float* p, bool in, float (&f)[8]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (in) x = __ldg(reinterpret_cast<const float4*>(p) + h);
-    f[4 * h] = x.x, f[4 * h + 1] = x.y, f[4 * h + 2] = x.z, f[4 * h + 3] = x.w;
-  }
 }
 
 template <int D>
@@ -389,13 +351,6 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         float s[kKT];
         tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
         tmem_ld32(tS + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
-        if (prm.out.logits && rvalid) {
-          // (scores are asked for in launches that are not pooled)
-          float* dst = prm.out.logits + ((int64_t)u.g * prm.rm.RG + r) * prm.a.S + t.j0;
-#pragma unroll
-          for (int i = 0; i < kKT; ++i)
-            if (i < t.n) dst[i] = s[i] * sl2;
-        }
         if (__any_sync(0xffffffffu, (sees0 & sees1) != 0xffffffffu)) {
 #pragma unroll
           for (int i = 0; i < kKT; ++i)
@@ -444,6 +399,7 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         const int64_t row = cache_row(prm.a, prm.rm, u.g, r).row;
         const int64_t at = (int64_t)(prm.out.slot0 + u.sp) * prm.out.rows + row;
         if (!prm.out.direct) prm.out.part_ml[at] = make_float2(m, l);
+        if (prm.out.lse) prm.out.lse[row] = l == 0.f ? INFINITY : m + log2f(l);
         const float mul = !prm.out.direct ? 1.f : l == 0.f ? 0.f : 1.f / l;
         float* dst = prm.out.direct ? static_cast<float*>(prm.a.o) + row * D
                                     : prm.out.part_o + at * D;

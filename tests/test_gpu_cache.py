@@ -278,6 +278,12 @@ CACHE = [
     (1, 4, 2, 33, 400, 128, [400]),
     (2, 4, 4, 130, 260, 64, [260, 129]),
     (1, 20, 1, 1, 150, 128, [140]),
+    (3, 8, 2, 8, 700, 128, [700, 300, 5]),
+    (1, 3, 1, 200, 1500, 64, [1400]),
+    (2, 4, 2, 256, 300, 128, [300, 129]),
+    (2, 24, 3, 70, 2000, 128, [2000, 1111]),
+    (1, 2, 2, 300, 300, 64, [300]),
+    (2, 18, 1, 1, 4100, 64, [4100, 0]),
 ]
 
 
