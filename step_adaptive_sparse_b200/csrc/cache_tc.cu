@@ -135,7 +135,7 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
           return false;
         if (lane == 0) {
           Unit u;
-          u.valid = decode_unit<128>((int)(blockIdx.x + k * gridDim.x), prm, u) ? 1 : 0;
+          u.valid = decode_unit<128>(unit_index(k), prm, u) ? 1 : 0;
           s_rec[slot] = u;
           mbar_arrive(bar(BAR_REC_FULL + slot));
         }
@@ -221,89 +221,99 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
-        uint32_t kv_it = 0, unit_count = 0;
-        uint32_t p_cnt[2] = {0, 0};
-        bool ok = true;
-        auto kv_addr = [&](uint32_t it) { return sbase + G::kSmemKV + (it % kStages) * G::kTileBytes; };
-        auto wait_kv = [&](uint32_t it) {
-          if (!mbar_wait(bar(BAR_KV_FULL + it % kStages), (it / kStages) & 1u, abort_flag))
-            return false;
-          if (s_copied[it % kStages]) fence_proxy_async();
-          return true;
-        };
-        auto qk = [&](int t, uint32_t ks) {
-          const uint32_t qs = sbase + t * G::kTileBytes, d = tmem + t * 128;
-  #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-            mma_ss(d, sdesc(qs + off, 16, 1024), sdesc(ks + off, 16, 1024), kIdescQK, kk > 0);
-          }
-          mma_commit(bar(BAR_S_FULL0 + t));
-        };
-        auto pv = [&](int t, uint32_t vs, bool first, bool last) -> bool {
-          const uint32_t d = tmem + 256 + t * 128, p = tmem + t * 128;
-          constexpr int kPer = 8 / kPParts;
-  #pragma unroll
-          for (int h = 0; h < kPParts; ++h) {
-            if (!mbar_wait(bar((h + 1 < kPParts ? BAR_P_PART0 : BAR_P_FULL0) + t), p_cnt[t] & 1u,
-                           abort_flag))
-              return false;
-            tc_fence_after();
-  #pragma unroll
-            for (int kk = kPer * h; kk < kPer * h + kPer; ++kk)
-              mma_ts(d, p + kk * 8, sdesc(vs + kk * 2048, kHalfBytes, 1024), kIdescPV,
-                     (first && kk == 0) ? 0u : 1u);
-          }
-          ++p_cnt[t];
-          if (last) mma_commit(bar(BAR_O_FULL0 + t));
-          return true;
-        };
-        while (ok) {
-          const uint32_t slot = unit_count % kRecSlots;
-          if (!(ok = mbar_wait(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u, abort_flag)))
-            break;
-          const Unit& u = s_rec[slot];
-          if (!u.valid) break;
-          const int nt = u.nt;
-          const TileRange a0 = tile_range(u, 0), a1 = tile_range(u, 1);
-          mbar_arrive(bar(BAR_REC_EMPTY + slot));
-          if (!(ok = mbar_wait(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
-          if (nt == 0) mma_commit(bar(BAR_Q_EMPTY));
-          if (nt > 0) {
-            if (!(ok = wait_kv(kv_it))) break;
-            tc_fence_after();
-            if (a0.has(0)) qk(0, kv_addr(kv_it));
-            if (a1.has(0)) qk(1, kv_addr(kv_it));
-            mma_commit(bar(BAR_KV_EMPTY + kv_it % kStages));
-            if (nt == 1) mma_commit(bar(BAR_Q_EMPTY));
-          }
-          for (int j = 0; j < nt; ++j) {
-            const uint32_t vi = kv_it + 2 * j + 1, kn = vi + 1;
-            const bool next = j + 1 < nt;
-            if (!(ok = wait_kv(vi))) break;
-            if (a0.has(j) && !(ok = pv(0, kv_addr(vi), j == a0.first, j == a0.last))) break;
-            if (next) {
-              if (!(ok = wait_kv(kn))) break;
-              tc_fence_after();
-              if (a0.has(j + 1)) qk(0, kv_addr(kn));
-            }
-            if (a1.has(j) && !(ok = pv(1, kv_addr(vi), j == a1.first, j == a1.last))) break;
-            mma_commit(bar(BAR_KV_EMPTY + vi % kStages));
-            if (next) {
-              if (a1.has(j + 1)) qk(1, kv_addr(kn));
-              mma_commit(bar(BAR_KV_EMPTY + kn % kStages));
-              if (j + 2 == nt) mma_commit(bar(BAR_Q_EMPTY));
-            }
-          }
-          kv_it += 2 * nt;
-          ++unit_count;
+      uint32_t kv_it = 0, unit_count = 0;
+      uint32_t p_cnt[2] = {0, 0};
+      bool ok = true;
+      const uint64_t dq = sdesc(sbase, 16, 1024), dk = sdesc(sbase + G::kSmemKV, 16, 1024);
+      const uint64_t dv = sdesc(sbase + G::kSmemKV, kHalfBytes, 1024);
+      auto wait_kv = [&](uint32_t it) {
+        if (!warp_wait_all(bar(BAR_KV_FULL + it % kStages), (it / kStages) & 1u, abort_flag))
+          return false;
+        if (s_copied[it % kStages]) fence_proxy_async();
+        return true;
+      };
+      auto qk = [&](int t, uint32_t it) {
+        const uint32_t d = tmem + t * 128, ks = it % kStages * G::kTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+          mma_ss_w(d, sdesc_at(dq, t * G::kTileBytes + off), sdesc_at(dk, ks + off), kIdescQK,
+                   kk > 0);
         }
-        int drain_abort = 0;
-        mma_commit(bar(BAR_DRAIN));
-        mbar_wait(bar(BAR_DRAIN), 0, &drain_abort);
+        mma_commit_w(bar(BAR_S_FULL0 + t));
+      };
+      auto pv = [&](int t, uint32_t it, bool first, bool last) -> bool {
+        const uint32_t d = tmem + 256 + t * 128, p = tmem + t * 128;
+        const uint32_t vs = it % kStages * G::kTileBytes;
+        constexpr int kPer = 8 / kPParts;
+#pragma unroll
+        for (int h = 0; h < kPParts; ++h) {
+          if (!warp_wait_all(bar((h + 1 < kPParts ? BAR_P_PART0 : BAR_P_FULL0) + t), p_cnt[t] & 1u,
+                             abort_flag))
+            return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = kPer * h; kk < kPer * h + kPer; ++kk)
+            mma_ts_w(d, p + kk * 8, sdesc_at(dv, vs + kk * 2048), kIdescPV,
+                     (first && kk == 0) ? 0u : 1u);
+        }
+        ++p_cnt[t];
+        if (last) mma_commit_w(bar(BAR_O_FULL0 + t));
+        return true;
+      };
+      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      while (ok) {
+        const uint32_t slot = unit_count % kRecSlots;
+        if (!(ok = warp_wait_all(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u,
+                                 abort_flag)))
+          break;
+        const Unit& u = s_rec[slot];
+        if (!uniform(u.valid)) break;
+        const int nt = uniform(u.nt);
+        TileRange ar[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const TileRange x = tile_range(u, t);
+          ar[t] = TileRange{uniform(x.lead), uniform(x.oa), uniform(x.ob), uniform(x.first),
+                            uniform(x.last)};
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_REC_EMPTY + slot));
+        __syncwarp();
+        if (!(ok = warp_wait_all(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
+        if (nt == 0) mma_commit_w(bar(BAR_Q_EMPTY));
+        if (nt > 0) {
+          if (!(ok = wait_kv(kv_it))) break;
+          tc_fence_after();
+          if (ar[0].has(0)) qk(0, kv_it);
+          if (ar[1].has(0)) qk(1, kv_it);
+          mma_commit_w(bar(BAR_KV_EMPTY + kv_it % kStages));
+          if (nt == 1) mma_commit_w(bar(BAR_Q_EMPTY));
+        }
+        for (int j = 0; j < nt; ++j) {
+          const uint32_t vi = kv_it + 2 * j + 1, kn = vi + 1;
+          const bool next = j + 1 < nt;
+          if (!(ok = wait_kv(vi))) break;
+          if (ar[0].has(j) && !(ok = pv(0, vi, j == ar[0].first, j == ar[0].last))) break;
+          if (next) {
+            if (!(ok = wait_kv(kn))) break;
+            tc_fence_after();
+            if (ar[0].has(j + 1)) qk(0, kn);
+          }
+          if (ar[1].has(j) && !(ok = pv(1, vi, j == ar[1].first, j == ar[1].last))) break;
+          mma_commit_w(bar(BAR_KV_EMPTY + vi % kStages));
+          if (next) {
+            if (ar[1].has(j + 1)) qk(1, kn);
+            mma_commit_w(bar(BAR_KV_EMPTY + kn % kStages));
+            if (j + 2 == nt) mma_commit_w(bar(BAR_Q_EMPTY));
+          }
+        }
+        kv_it += 2 * nt;
+        ++unit_count;
       }
-      __syncwarp();
+      int drain_abort = 0;
+      mma_commit_w(bar(BAR_DRAIN));
+      warp_wait_all(bar(BAR_DRAIN), 0, &drain_abort);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh) : "memory");

@@ -36,7 +36,7 @@ constexpr int kRecSlots = 3;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // The other warpgroups get what the product warpgroup gives up; the sum is
 // exactly the allocation of a 168-register launch (checked before it).
-constexpr int kRegsRead = 192, kRegsMma = 56, kRegsSoft = 256;
+constexpr int kRegsRead = 192, kRegsMma = 64, kRegsSoft = 248;
 static_assert(kRegsRead + kRegsMma + kRegsSoft == 3 * 168, "register split");
 
 template <int D>
@@ -131,7 +131,7 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         return false;
       if (lane == 0) {
         Unit u;
-        u.valid = decode_unit<kKT>((int)(blockIdx.x + k * gridDim.x), prm, u) ? 1 : 0;
+        u.valid = decode_unit<kKT>(unit_index(k), prm, u) ? 1 : 0;
         s_rec[slot] = u;
         mbar_arrive(bar(BAR_REC_FULL + slot));
       }
@@ -215,72 +215,75 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma) : "memory");
     // -------------------------------------------------------------- products
-    if (warp == 4 && lane == 0) {
+    if (warp == 4) {
       uint32_t unit_count = 0;
       uint32_t s_it = 0, p_it = 0;     // tiles whose scores, whose outputs have been issued
       bool ok = true;
+      const uint64_t dq = sdesc(sbase, 16, 1024), dk = sdesc(sbase + G::kSmemK, 16, 1024);
+      const uint64_t dv = sdesc(sbase + G::kSmemV, G::kKHalf, 1024);
       auto qk = [&]() -> bool {
-        if (!mbar_wait(bar(BAR_K_FULL), s_it & 1u, abort_flag)) return false;
+        if (!warp_wait_all(bar(BAR_K_FULL), s_it & 1u, abort_flag)) return false;
         tc_fence_after();
         const uint32_t d = tmem + (s_it & 1u) * 64;
 #pragma unroll 1
         for (int t = 0; t < 6; ++t) {
-          const uint32_t qs = sbase + kPartA[t] * G::kQTerm;
-          const uint32_t ks = sbase + G::kSmemK + kPartB[t] * G::kKTerm;
+          const uint32_t qs = part_a(t) * G::kQTerm, ks = part_b(t) * G::kKTerm;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(d, sdesc(qs + (kk >> 2) * G::kQHalf + (kk & 3) * 32, 16, 1024),
-                   sdesc(ks + (kk >> 2) * G::kKHalf + (kk & 3) * 32, 16, 1024), kIdescS,
-                   (t > 0 || kk > 0) ? 1u : 0u);
+            mma_ss_w(d, sdesc_at(dq, qs + (kk >> 2) * G::kQHalf + (kk & 3) * 32),
+                     sdesc_at(dk, ks + (kk >> 2) * G::kKHalf + (kk & 3) * 32), kIdescS,
+                     (t > 0 || kk > 0) ? 1u : 0u);
         }
-        mma_commit(bar(BAR_S_FULL0 + (s_it & 1u)));
-        mma_commit(bar(BAR_K_EMPTY));
+        mma_commit_w(bar(BAR_S_FULL0 + (s_it & 1u)));
+        mma_commit_w(bar(BAR_K_EMPTY));
         ++s_it;
         return true;
       };
       auto pv = [&]() -> bool {
         const uint32_t b = p_it & 1u, ph = (p_it >> 1) & 1u;
-        if (!mbar_wait(bar(BAR_V_FULL), p_it & 1u, abort_flag)) return false;
-        if (!mbar_wait(bar(BAR_P_FULL0 + b), ph, abort_flag)) return false;
+        if (!warp_wait_all(bar(BAR_V_FULL), p_it & 1u, abort_flag)) return false;
+        if (!warp_wait_all(bar(BAR_P_FULL0 + b), ph, abort_flag)) return false;
         tc_fence_after();
         const uint32_t d = tmem + kColO + b * D;
 #pragma unroll 1
         for (int t = 0; t < 6; ++t) {
-          const int pa = kPartA[t];
+          const uint32_t pa = part_a(t);
           const uint32_t p = tmem + (pa < 2 ? b * 64 + pa * 32 : kColX + b * 32);
-          const uint32_t vs = sbase + G::kSmemV + kPartB[t] * G::kKTerm;
 #pragma unroll
           for (int kk = 0; kk < kKT / 16; ++kk)
-            mma_ts(d, p + kk * 8, sdesc(vs + kk * 2048, G::kKHalf, 1024), kIdescO,
-                   (t > 0 || kk > 0) ? 1u : 0u);
+            mma_ts_w(d, p + kk * 8, sdesc_at(dv, part_b(t) * G::kKTerm + kk * 2048), kIdescO,
+                     (t > 0 || kk > 0) ? 1u : 0u);
         }
-        mma_commit(bar(BAR_O_FULL0 + b));
-        mma_commit(bar(BAR_V_EMPTY));
+        mma_commit_w(bar(BAR_O_FULL0 + b));
+        mma_commit_w(bar(BAR_V_EMPTY));
         ++p_it;
         return true;
       };
       while (ok) {
         const uint32_t slot = unit_count % kRecSlots;
-        if (!(ok = mbar_wait(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u, abort_flag)))
+        if (!(ok = warp_wait_all(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u,
+                                 abort_flag)))
           break;
-        const int valid = s_rec[slot].valid, nt = s_rec[slot].nt;
-        mbar_arrive(bar(BAR_REC_EMPTY + slot));
+        const int valid = __shfl_sync(0xffffffffu, s_rec[slot].valid, 0);
+        const int nt = __shfl_sync(0xffffffffu, s_rec[slot].nt, 0);
+        if (lane == 0) mbar_arrive(bar(BAR_REC_EMPTY + slot));
+        __syncwarp();
         if (!valid) break;
-        if (!(ok = mbar_wait(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
-        if (nt == 0) mma_commit(bar(BAR_Q_EMPTY));
+        if (!(ok = warp_wait_all(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
+        if (nt == 0) mma_commit_w(bar(BAR_Q_EMPTY));
         for (int j = 0; j < nt; ++j) {
           if (j == 0 && !(ok = qk())) break;
           if (j + 1 < nt && !(ok = qk())) break;
           if (j == (nt > 1 ? nt - 2 : 0))
-            mma_commit(bar(BAR_Q_EMPTY));              // the unit's scores are all issued
+            mma_commit_w(bar(BAR_Q_EMPTY));            // the unit's scores are all issued
           if (!(ok = pv())) break;
         }
         if (!ok) break;
         ++unit_count;
       }
       int drain_abort = 0;
-      mma_commit(bar(BAR_DRAIN));
-      mbar_wait(bar(BAR_DRAIN), 0, &drain_abort);
+      mma_commit_w(bar(BAR_DRAIN));
+      warp_wait_all(bar(BAR_DRAIN), 0, &drain_abort);
     }
     __syncwarp();
   } else {

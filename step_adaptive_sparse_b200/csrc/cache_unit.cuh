@@ -90,6 +90,12 @@ __host__ __device__ __forceinline__ TileRange tile_range(const Unit& u, int t) {
   return TileRange{u.lead[t], u.oa[t], u.ob[t], first_tile(u, t), last_tile(u, t)};
 }
 
+// The k-th unit of a block: the blocks take units in turn, there and back, so
+// that units in the order of their cost come out even.
+__device__ __forceinline__ int unit_index(uint32_t k) {
+  return (int)(k * gridDim.x + (k & 1u ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
+}
+
 // Unit idx of a launch; false behind the last one.
 template <int KT>
 __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& u) {

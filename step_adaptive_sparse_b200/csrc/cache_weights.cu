@@ -169,31 +169,30 @@ cache_weights_tc_kernel(const __grid_constant__ WMaps tm, const __grid_constant_
         mbar_wait(bar(W_Q_FULL + (x & 1u)), (x >> 1) & 1u, &drain_abort);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       uint32_t it = 0;
-      bool ok = nrt == 0 || mbar_wait(bar(W_K_FULL), 0, abort_flag);
+      const uint64_t dk = sdesc(sbase, 16, 1024), dq = sdesc(sbase + G::kSmemQ, 16, 1024);
+      bool ok = nrt == 0 || warp_wait_all(bar(W_K_FULL), 0, abort_flag);
       for (int t = 0; t < nrt && ok; ++t) {
         if (row_tile<128>(p.a, p.R, len, t).hi1 <= j0) continue;
         const uint32_t b = it & 1u, ph = (it >> 1) & 1u;
-        if (!(ok = mbar_wait(bar(W_Q_FULL + b), ph, abort_flag))) break;
-        if (!(ok = mbar_wait(bar(W_S_EMPTY + b), ph ^ 1u, abort_flag))) break;
+        if (!(ok = warp_wait_all(bar(W_Q_FULL + b), ph, abort_flag))) break;
+        if (!(ok = warp_wait_all(bar(W_S_EMPTY + b), ph ^ 1u, abort_flag))) break;
         tc_fence_after();
-        const uint32_t qs = sbase + G::kSmemQ + b * G::kTileBytes;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-          mma_ss(tmem + b * 128, sdesc(sbase + off, 16, 1024), sdesc(qs + off, 16, 1024), kIdescQK,
-                 kk > 0);
+          mma_ss_w(tmem + b * 128, sdesc_at(dk, off), sdesc_at(dq, b * G::kTileBytes + off),
+                   kIdescQK, kk > 0);
         }
-        mma_commit(bar(W_S_FULL + b));
-        mma_commit(bar(W_Q_EMPTY + b));
+        mma_commit_w(bar(W_S_FULL + b));
+        mma_commit_w(bar(W_Q_EMPTY + b));
         ++it;
       }
       int drain_abort = 0;
-      mma_commit(bar(W_DRAIN));
-      mbar_wait(bar(W_DRAIN), 0, &drain_abort);
+      mma_commit_w(bar(W_DRAIN));
+      warp_wait_all(bar(W_DRAIN), 0, &drain_abort);
     }
-    __syncwarp();
   } else if (warp >= 4) {
     // group grp takes every second tile
     const uint32_t grp = (uint32_t)(warp - 4) >> 2;
@@ -333,34 +332,33 @@ cache_weights_tc32_kernel(const __grid_constant__ WParams p) {
       }
     }
   } else if (warp == 4) {
-    if (lane == 0) {
+    {
       uint32_t it = 0;
-      bool ok = nrt == 0 || mbar_wait(bar(W_K_FULL), 0, abort_flag);
+      const uint64_t dk = sdesc(sbase, 16, 1024), dq = sdesc(sbase + G::kSmemQ, 16, 1024);
+      bool ok = nrt == 0 || warp_wait_all(bar(W_K_FULL), 0, abort_flag);
       for (int t = 0; t < nrt && ok; ++t) {
         if (row_tile<kKR32>(p.a, p.R, len, t).hi1 <= j0) continue;
         const uint32_t b = it & 1u, ph = (it >> 1) & 1u;
-        if (!(ok = mbar_wait(bar(W_Q_FULL + b), ph, abort_flag))) break;
-        if (!(ok = mbar_wait(bar(W_S_EMPTY + b), ph ^ 1u, abort_flag))) break;
+        if (!(ok = warp_wait_all(bar(W_Q_FULL + b), ph, abort_flag))) break;
+        if (!(ok = warp_wait_all(bar(W_S_EMPTY + b), ph ^ 1u, abort_flag))) break;
         tc_fence_after();
-#pragma unroll 1
+#pragma unroll
         for (int x = 0; x < 6; ++x) {
-          const uint32_t ks = sbase + kPartA[x] * G::kKTerm;
-          const uint32_t qs = sbase + G::kSmemQ + (b * 3 + kPartB[x]) * G::kQTerm;
+          const uint32_t ks = part_a(x) * G::kKTerm, qs = (b * 3 + part_b(x)) * G::kQTerm;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + b * kKR32, sdesc(ks + (kk >> 2) * G::kKHalf + (kk & 3) * 32, 16, 1024),
-                   sdesc(qs + (kk >> 2) * G::kQHalf + (kk & 3) * 32, 16, 1024),
-                   idesc(kKR32, false), (x > 0 || kk > 0) ? 1u : 0u);
+            mma_ss_w(tmem + b * kKR32, sdesc_at(dk, ks + (kk >> 2) * G::kKHalf + (kk & 3) * 32),
+                     sdesc_at(dq, qs + (kk >> 2) * G::kQHalf + (kk & 3) * 32), idesc(kKR32, false),
+                     (x > 0 || kk > 0) ? 1u : 0u);
         }
-        mma_commit(bar(W_S_FULL + b));
-        mma_commit(bar(W_Q_EMPTY + b));
+        mma_commit_w(bar(W_S_FULL + b));
+        mma_commit_w(bar(W_Q_EMPTY + b));
         ++it;
       }
       int drain_abort = 0;
-      mma_commit(bar(W_DRAIN));
-      mbar_wait(bar(W_DRAIN), 0, &drain_abort);
+      mma_commit_w(bar(W_DRAIN));
+      warp_wait_all(bar(W_DRAIN), 0, &drain_abort);
     }
-    __syncwarp();
   } else if (warp >= 8) {
     const int th = ((warp & 3) << 5) + lane;         // TMEM lane = key of the block
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) << 5) << 16);

@@ -8,8 +8,8 @@ namespace area {
 namespace {
 
 // The order of the six terms: parts of the first and of the second factor.
-__device__ __constant__ const int kPartA[6] = {1, 0, 2, 0, 1, 0};
-__device__ __constant__ const int kPartB[6] = {1, 2, 0, 1, 0, 0};
+__device__ __forceinline__ constexpr uint32_t part_a(int t) { return 0x102010u >> (4 * (5 - t)) & 3u; }
+__device__ __forceinline__ constexpr uint32_t part_b(int t) { return 0x120100u >> (4 * (5 - t)) & 3u; }
 
 // The top parts of two values, packed (a in the low half); what is left of the
 // values takes their place.
@@ -37,6 +37,7 @@ __device__ __forceinline__ void put8(uint32_t at, int term, float (&f)[8]) {
     st_shared16(at + t * term, w);
   }
 }
+// Eight values of a row, or zeros.
 __device__ __forceinline__ void get8(const float* p, bool in, float (&f)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
