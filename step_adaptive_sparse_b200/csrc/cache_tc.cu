@@ -230,17 +230,25 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
         if (!warp_wait_all(bar(BAR_KV_FULL + it % kStages), (it / kStages) & 1u, abort_flag))
           return false;
         if (s_copied[it % kStages]) fence_proxy_async();
+        tc_fence_after();
         return true;
+      };
+      auto commit = [&](uint32_t b) {
+        if (elect_one()) mma_commit(b);
+        __syncwarp();
       };
       auto qk = [&](int t, uint32_t it) {
         const uint32_t d = tmem + t * 128, ks = it % kStages * G::kTileBytes;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-          mma_ss_w(d, sdesc_at(dq, t * G::kTileBytes + off), sdesc_at(dk, ks + off), kIdescQK,
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+            mma_ss(d, sdesc_at(dq, t * G::kTileBytes + off), sdesc_at(dk, ks + off), kIdescQK,
                    kk > 0);
+          }
+          mma_commit(bar(BAR_S_FULL0 + t));
         }
-        mma_commit_w(bar(BAR_S_FULL0 + t));
+        __syncwarp();
       };
       auto pv = [&](int t, uint32_t it, bool first, bool last) -> bool {
         const uint32_t d = tmem + 256 + t * 128, p = tmem + t * 128;
@@ -252,13 +260,16 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
                              abort_flag))
             return false;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = kPer * h; kk < kPer * h + kPer; ++kk)
-            mma_ts_w(d, p + kk * 8, sdesc_at(dv, vs + kk * 2048), kIdescPV,
+            for (int kk = kPer * h; kk < kPer * h + kPer; ++kk)
+              mma_ts(d, p + kk * 8, sdesc_at(dv, vs + kk * 2048), kIdescPV,
                      (first && kk == 0) ? 0u : 1u);
+            if (last && h + 1 == kPParts) mma_commit(bar(BAR_O_FULL0 + t));
+          }
+          __syncwarp();
         }
         ++p_cnt[t];
-        if (last) mma_commit_w(bar(BAR_O_FULL0 + t));
         return true;
       };
       auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
@@ -281,38 +292,38 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
         if (lane == 0) mbar_arrive(bar(BAR_REC_EMPTY + slot));
         __syncwarp();
         if (!(ok = warp_wait_all(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
-        if (nt == 0) mma_commit_w(bar(BAR_Q_EMPTY));
+        if (nt == 0) commit(bar(BAR_Q_EMPTY));
         if (nt > 0) {
           if (!(ok = wait_kv(kv_it))) break;
-          tc_fence_after();
           if (ar[0].has(0)) qk(0, kv_it);
           if (ar[1].has(0)) qk(1, kv_it);
-          mma_commit_w(bar(BAR_KV_EMPTY + kv_it % kStages));
-          if (nt == 1) mma_commit_w(bar(BAR_Q_EMPTY));
+          commit(bar(BAR_KV_EMPTY + kv_it % kStages));
+          if (nt == 1) commit(bar(BAR_Q_EMPTY));
         }
+        // the tiles of the next step are waited for before this step's weights
+        // are: their loads are long done, so that no wait comes between a tile's
+        // products
+        if (nt > 0 && !(ok = wait_kv(kv_it + 1))) break;
         for (int j = 0; j < nt; ++j) {
           const uint32_t vi = kv_it + 2 * j + 1, kn = vi + 1;
           const bool next = j + 1 < nt;
-          if (!(ok = wait_kv(vi))) break;
+          if (next && !(ok = wait_kv(kn))) break;
           if (ar[0].has(j) && !(ok = pv(0, vi, j == ar[0].first, j == ar[0].last))) break;
-          if (next) {
-            if (!(ok = wait_kv(kn))) break;
-            tc_fence_after();
-            if (ar[0].has(j + 1)) qk(0, kn);
-          }
+          if (next && ar[0].has(j + 1)) qk(0, kn);
           if (ar[1].has(j) && !(ok = pv(1, vi, j == ar[1].first, j == ar[1].last))) break;
-          mma_commit_w(bar(BAR_KV_EMPTY + vi % kStages));
+          if (next && ar[1].has(j + 1)) qk(1, kn);
+          commit(bar(BAR_KV_EMPTY + vi % kStages));
           if (next) {
-            if (ar[1].has(j + 1)) qk(1, kn);
-            mma_commit_w(bar(BAR_KV_EMPTY + kn % kStages));
-            if (j + 2 == nt) mma_commit_w(bar(BAR_Q_EMPTY));
+            commit(bar(BAR_KV_EMPTY + kn % kStages));
+            if (j + 2 == nt) commit(bar(BAR_Q_EMPTY));
+            if (!(ok = wait_kv(kn + 1))) break;
           }
         }
         kv_it += 2 * nt;
         ++unit_count;
       }
       int drain_abort = 0;
-      mma_commit_w(bar(BAR_DRAIN));
+      commit(bar(BAR_DRAIN));
       warp_wait_all(bar(BAR_DRAIN), 0, &drain_abort);
     }
   } else {

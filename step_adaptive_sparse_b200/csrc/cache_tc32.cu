@@ -12,15 +12,18 @@
 // a chain is kept short: one tile's scores, or one tile's 64 keys times their
 // values, whose sum is added in registers with the running output.
 //
-// A persistent CTA per SM of 384 threads: warps 0-3 read keys, values and
-// queries, cut them into their parts and write these as swizzled operand tiles
-// (rows past the list as zeros, so that nothing outside it is read); warp 4
-// issues the products; warps 8-11 do the softmax of one tile of 128 query rows
-// and hold its output, one row to a thread.  TMEM: S0 | S1 (64 columns each;
-// the weights' first two parts replace a tile's scores) | X0 | X1 (32 each, the
-// third part) | O0 | O1 (one tile's output, D each).  Products are issued as
-// QK(j + 1), PV(j), so that a tile's softmax runs under the other products; the
-// next keys are cut up while PV runs and the next values while QK does.
+// A persistent CTA per SM of 512 threads: warps 0-7 read keys and values, cut
+// them into their parts and write these as swizzled operand tiles (rows past
+// the list as zeros, so that nothing outside it is read), two buffers each;
+// warp 8 issues the products, warp 9 decodes work units; warps 12-15 hold one tile of 128 query rows, one
+// row to a thread: they cut the queries, do the softmax and hold the output.
+// Both products take their first factor from TMEM, so that shared memory, which
+// also takes the parts' writes, feeds the tensor cores with the second alone
+// (queries in shared memory: 7000 cycles a tile at D = 128).  TMEM: S0 | S1 (64
+// columns each; the weights' first two parts replace a tile's scores) | X0 | X1
+// (32 each, the third part) | Q (three parts of D / 2) | O (one tile's output).
+// Products are issued as QK(j + 1), PV(j), so that a tile's softmax and the
+// reading of its output run under the other products.
 // Work units and the keys of a row are as in the bf16 kernel, with one row tile
 // and key tiles of 64.  Every mbarrier wait is bounded.
 #include "cache_unit.cuh"
@@ -30,30 +33,33 @@
 namespace area {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512, kReadWarps = 8, kReadThreads = 32 * kReadWarps;
 constexpr int kKT = 64;                    // keys of a tile
 constexpr int kRecSlots = 3;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-// The other warpgroups get what the product warpgroup gives up; the sum is
-// exactly the allocation of a 168-register launch (checked before it).
-constexpr int kRegsRead = 192, kRegsMma = 64, kRegsSoft = 248;
-static_assert(kRegsRead + kRegsMma + kRegsSoft == 3 * 168, "register split");
+// The softmax warpgroup gets what the others give up; the sum is exactly the
+// allocation of a 128-register launch (checked before it).
+constexpr int kRegsRead = 96, kRegsMma = 72, kRegsSoft = 248;
+static_assert(2 * kRegsRead + kRegsMma + kRegsSoft == 4 * 128, "register split");
 
 template <int D>
 struct Geo {
   static constexpr int kHalves = D / 64;
-  static constexpr int kQHalf = 128 * 128, kKHalf = kKT * 128;   // bytes of 64 columns
-  static constexpr int kQTerm = kHalves * kQHalf, kKTerm = kHalves * kKHalf;
-  static constexpr int kSmemK = 3 * kQTerm, kSmemV = kSmemK + 3 * kKTerm;
-  static constexpr int kSmemBar = kSmemV + 3 * kKTerm;
+  static constexpr int kHalf = kKT * 128;                        // bytes of 64 columns
+  static constexpr int kTerm = kHalves * kHalf, kTile = 3 * kTerm;
+  static constexpr int kSmemV = 2 * kTile, kSmemBar = kSmemV + 2 * kTile;
   static constexpr int kSmemBytes = kSmemBar + 256 + 1024;       // barriers + alignment slack
-  static_assert(kSmemBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
+  static_assert(kSmemBytes + 2048 <= 227 * 1024, "shared memory of one CTA");
+  static constexpr uint32_t kColX = 128, kColQ = 192, kColO = kColQ + 3 * D / 2;
+  static_assert(kColO + D <= 512, "TMEM");
 };
 
 enum {
-  BAR_Q_FULL = 0, BAR_Q_EMPTY, BAR_K_FULL, BAR_K_EMPTY, BAR_V_FULL, BAR_V_EMPTY,
-  BAR_S_FULL0, BAR_S_FULL1, BAR_P_FULL0, BAR_P_FULL1, BAR_O_FULL0, BAR_O_FULL1,
-  BAR_REC_FULL,
+  BAR_Q_FULL = 0, BAR_O_FULL, BAR_O_EMPTY,
+  BAR_K_FULL, BAR_K_EMPTY = BAR_K_FULL + 2,
+  BAR_V_FULL = BAR_K_EMPTY + 2, BAR_V_EMPTY = BAR_V_FULL + 2,
+  BAR_S_FULL = BAR_V_EMPTY + 2, BAR_P_FULL = BAR_S_FULL + 2,
+  BAR_REC_FULL = BAR_P_FULL + 2,
   BAR_REC_EMPTY = BAR_REC_FULL + kRecSlots,
   BAR_DRAIN = BAR_REC_EMPTY + kRecSlots,
   BAR_COUNT
@@ -69,8 +75,6 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
   using G = Geo<D>;
-  constexpr int kChunks = D / 8;                  // 32-byte pieces of a row of fp32
-  constexpr int kPer = kKT * kChunks / 128;       // pieces of a thread and key tile
   constexpr uint32_t kIdescS = idesc(kKT, false), kIdescO = idesc(D, true);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -81,30 +85,31 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
   __shared__ int s_abort;
   __shared__ __align__(16) Unit s_rec[kRecSlots];
   __shared__ KeySpan s_span[128];          // of the softmax threads' rows
-  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  auto bar = [&](uint32_t i) { return bar0 + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     s_abort = 0;
     mbar_init(bar(BAR_Q_FULL), 128);
-    mbar_init(bar(BAR_Q_EMPTY), 1);
-    mbar_init(bar(BAR_K_FULL), 128);
-    mbar_init(bar(BAR_K_EMPTY), 1);
-    mbar_init(bar(BAR_V_FULL), 128);
-    mbar_init(bar(BAR_V_EMPTY), 1);
+    mbar_init(bar(BAR_O_FULL), 1);
+    mbar_init(bar(BAR_O_EMPTY), 128);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(BAR_S_FULL0 + t), 1);
-      mbar_init(bar(BAR_P_FULL0 + t), 128);
-      mbar_init(bar(BAR_O_FULL0 + t), 1);
+      mbar_init(bar(BAR_K_FULL + t), kReadThreads);
+      mbar_init(bar(BAR_K_EMPTY + t), 1);
+      mbar_init(bar(BAR_V_FULL + t), kReadThreads);
+      mbar_init(bar(BAR_V_EMPTY + t), 1);
+      mbar_init(bar(BAR_S_FULL + t), 1);
+      mbar_init(bar(BAR_P_FULL + t), 128);
     }
     for (int s = 0; s < kRecSlots; ++s) {
       mbar_init(bar(BAR_REC_FULL + s), 1);
-      mbar_init(bar(BAR_REC_EMPTY + s), 8);   // warps 1-3, the MMA thread, 4 softmax warps
+      // the reading warps, the product warp, four softmax warps
+      mbar_init(bar(BAR_REC_EMPTY + s), kReadWarps + 5);
     }
     mbar_init(bar(BAR_DRAIN), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 4) {
+  if (warp == kReadWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_u32(&s_tmem_base))
                  : "memory");
@@ -114,31 +119,17 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem_base;
-  constexpr uint32_t kColX = 128, kColO = 192;
   int* abort_flag = &s_abort;
 
   // the paths must not meet again before the end (see the bf16 kernel)
-  if (warp < 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRead) : "memory");
+  if (warp < kReadWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRead) : "memory");
     // ---------------------------------------------- reading and cutting up
-    const int tid = threadIdx.x, ch = tid % kChunks, row0 = tid / kChunks;
-    constexpr int kRowStep = 128 / kChunks;
+    constexpr int kPieces = D / 4;                  // 16-byte pieces of a row
+    constexpr int kRowStep = kReadThreads / kPieces, kPer = kKT / kRowStep;
+    const int piece = threadIdx.x % kPieces, row0 = threadIdx.x / kPieces;
     uint32_t k_it = 0, v_it = 0, unit_count = 0;
     bool ok = true;
-    auto publish = [&](uint32_t k) -> bool {
-      const uint32_t slot = k % kRecSlots;
-      if (!warp_wait0(bar(BAR_REC_EMPTY + slot), ((k / kRecSlots) & 1u) ^ 1u, abort_flag))
-        return false;
-      if (lane == 0) {
-        Unit u;
-        u.valid = decode_unit<kKT>(unit_index(k), prm, u) ? 1 : 0;
-        s_rec[slot] = u;
-        mbar_arrive(bar(BAR_REC_FULL + slot));
-      }
-      __syncwarp();
-      return true;
-    };
-    if (warp == 0) ok = publish(0);
     while (ok) {
       const uint32_t slot = unit_count % kRecSlots;
       if (!(ok = warp_wait_all(bar(BAR_REC_FULL + slot), (unit_count / kRecSlots) & 1u,
@@ -146,116 +137,103 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         break;
       const Unit& u = s_rec[slot];
       if (!u.valid) break;
-      if (warp == 0 && !(ok = publish(unit_count + 1))) break;
       const int nt = u.nt;
-      float kf[kPer][8], vf[kPer][8];
-      auto load = [&](float (&f)[kPer][8], int j, bool val) {
+      float kf[kPer][4], vf[kPer][4];
+      auto load = [&](float (&f)[kPer][4], int j, bool val) {
         const Tile t = tile_of<kKT>(u, j);
-        const float* base = static_cast<const float*>(t.kind ? (val ? prm.a.v : prm.a.k)
-                                                             : (val ? prm.a.vp : prm.a.kp)) +
-                            ((int64_t)(t.kind ? u.kvh : u.ph) * (t.kind ? prm.a.S : prm.a.P) +
-                             t.j0) * D + ch * 8;
+        const float* p = static_cast<const float*>(t.kind ? (val ? prm.a.v : prm.a.k)
+                                                          : (val ? prm.a.vp : prm.a.kp)) +
+                         ((int64_t)(t.kind ? u.kvh : u.ph) * (t.kind ? prm.a.S : prm.a.P) + t.j0 +
+                          row0) * D + piece * 4;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int r = row0 + i * kRowStep;
-          get8(base + (int64_t)r * D, r < t.n, f[i]);
-        }
+        for (int i = 0; i < kPer; ++i) get4(p + i * kRowStep * D, row0 + i * kRowStep < t.n, f[i]);
       };
-      auto put = [&](float (&f)[kPer][8], int at) {
+      auto put = [&](float (&f)[kPer][4], uint32_t at) {
+        at += sbase + (piece >> 4) * G::kHalf + (piece & 1) * 8;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int r = row0 + i * kRowStep;
-          put8(sbase + at + (ch >> 3) * G::kKHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-               G::kKTerm, f[i]);
+          put4(at + r * 128 + ((((piece >> 1) & 7) ^ (r & 7)) << 4), G::kTerm, f[i]);
         }
         fence_proxy_async();
       };
       if (nt > 0) load(kf, 0, false);
-      // queries
-      if (!(ok = warp_wait_all(bar(BAR_Q_EMPTY), (unit_count & 1u) ^ 1u, abort_flag))) break;
-#pragma unroll 1
-      for (int i0 = 0; i0 < kChunks; i0 += kPer) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int rr = u.r0[0] + row0 + (i0 + i) * kRowStep;
-          const bool in = rr < prm.rm.RG;
-          const int64_t row = in ? cache_row(prm.a, prm.rm, u.g, rr).row : 0;
-          get8(static_cast<const float*>(prm.a.q) + row * D + ch * 8, in, vf[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int r = row0 + (i0 + i) * kRowStep;
-          put8(sbase + (ch >> 3) * G::kQHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4), G::kQTerm,
-               vf[i]);
-        }
-      }
-      fence_proxy_async();
-      mbar_arrive(bar(BAR_Q_FULL));
       // K(j + 1) before V(j): the order in which their buffers become free
       for (int j = -1; j < nt; ++j) {
         if (j + 1 < nt) {
-          if (!(ok = warp_wait_all(bar(BAR_K_EMPTY), (k_it & 1u) ^ 1u, abort_flag))) break;
-          put(kf, G::kSmemK);
-          mbar_arrive(bar(BAR_K_FULL));
+          const uint32_t b = k_it & 1u;
+          if (!(ok = warp_wait_all(bar(BAR_K_EMPTY + b), ((k_it >> 1) & 1u) ^ 1u, abort_flag)))
+            break;
+          put(kf, b * G::kTile);
+          mbar_arrive(bar(BAR_K_FULL + b));
           ++k_it;
           if (j + 2 < nt) load(kf, j + 2, false);
         }
         if (j >= 0) {
-          if (!(ok = warp_wait_all(bar(BAR_V_EMPTY), (v_it & 1u) ^ 1u, abort_flag))) break;
-          put(vf, G::kSmemV);
-          mbar_arrive(bar(BAR_V_FULL));
+          const uint32_t b = v_it & 1u;
+          if (!(ok = warp_wait_all(bar(BAR_V_EMPTY + b), ((v_it >> 1) & 1u) ^ 1u, abort_flag)))
+            break;
+          put(vf, G::kSmemV + b * G::kTile);
+          mbar_arrive(bar(BAR_V_FULL + b));
           ++v_it;
         }
         if (j + 1 < nt) load(vf, j + 1, true);
       }
       if (!ok) break;
-      if (warp != 0 && lane == 0) mbar_arrive(bar(BAR_REC_EMPTY + slot));
+      if (lane == 0) mbar_arrive(bar(BAR_REC_EMPTY + slot));
       ++unit_count;
     }
-  } else if (warp < 8) {
+  } else if (warp < kReadWarps + 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma) : "memory");
     // -------------------------------------------------------------- products
-    if (warp == 4) {
+    if (warp == kReadWarps) {
       uint32_t unit_count = 0;
       uint32_t s_it = 0, p_it = 0;     // tiles whose scores, whose outputs have been issued
       bool ok = true;
-      const uint64_t dq = sdesc(sbase, 16, 1024), dk = sdesc(sbase + G::kSmemK, 16, 1024);
-      const uint64_t dv = sdesc(sbase + G::kSmemV, G::kKHalf, 1024);
+      const uint64_t dk = sdesc(sbase, 16, 1024), dv = sdesc(sbase + G::kSmemV, G::kHalf, 1024);
       auto qk = [&]() -> bool {
-        if (!warp_wait_all(bar(BAR_K_FULL), s_it & 1u, abort_flag)) return false;
+        const uint32_t b = s_it & 1u;
+        if (!warp_wait_all(bar(BAR_K_FULL + b), (s_it >> 1) & 1u, abort_flag)) return false;
         tc_fence_after();
-        const uint32_t d = tmem + (s_it & 1u) * 64;
-#pragma unroll 1
-        for (int t = 0; t < 6; ++t) {
-          const uint32_t qs = part_a(t) * G::kQTerm, ks = part_b(t) * G::kKTerm;
+        const uint32_t d = tmem + b * 64;
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss_w(d, sdesc_at(dq, qs + (kk >> 2) * G::kQHalf + (kk & 3) * 32),
-                     sdesc_at(dk, ks + (kk >> 2) * G::kKHalf + (kk & 3) * 32), kIdescS,
-                     (t > 0 || kk > 0) ? 1u : 0u);
+          for (int t = 0; t < 6; ++t) {
+            const uint32_t tq = tmem + G::kColQ + part_a(t) * (D / 2);
+            const uint64_t tk = opaque(sdesc_at(dk, b * G::kTile + part_b(t) * G::kTerm));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ts(d, tq + kk * 8, sdesc_at(tk, (kk >> 2) * G::kHalf + (kk & 3) * 32), kIdescS,
+                       (t > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(bar(BAR_S_FULL + b));
+          mma_commit(bar(BAR_K_EMPTY + b));
         }
-        mma_commit_w(bar(BAR_S_FULL0 + (s_it & 1u)));
-        mma_commit_w(bar(BAR_K_EMPTY));
+        __syncwarp();
         ++s_it;
         return true;
       };
       auto pv = [&]() -> bool {
         const uint32_t b = p_it & 1u, ph = (p_it >> 1) & 1u;
-        if (!warp_wait_all(bar(BAR_V_FULL), p_it & 1u, abort_flag)) return false;
-        if (!warp_wait_all(bar(BAR_P_FULL0 + b), ph, abort_flag)) return false;
+        if (!warp_wait_all(bar(BAR_V_FULL + b), ph, abort_flag)) return false;
+        if (!warp_wait_all(bar(BAR_P_FULL + b), ph, abort_flag)) return false;
+        if (!warp_wait_all(bar(BAR_O_EMPTY), (p_it & 1u) ^ 1u, abort_flag)) return false;
         tc_fence_after();
-        const uint32_t d = tmem + kColO + b * D;
-#pragma unroll 1
-        for (int t = 0; t < 6; ++t) {
-          const uint32_t pa = part_a(t);
-          const uint32_t p = tmem + (pa < 2 ? b * 64 + pa * 32 : kColX + b * 32);
+        const uint32_t d = tmem + G::kColO;
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kKT / 16; ++kk)
-            mma_ts_w(d, p + kk * 8, sdesc_at(dv, part_b(t) * G::kKTerm + kk * 2048), kIdescO,
-                     (t > 0 || kk > 0) ? 1u : 0u);
+          for (int t = 0; t < 6; ++t) {
+            const uint32_t pa = part_a(t);
+            const uint32_t p = tmem + (pa < 2 ? b * 64 + pa * 32 : G::kColX + b * 32);
+            const uint64_t tv = opaque(sdesc_at(dv, b * G::kTile + part_b(t) * G::kTerm));
+#pragma unroll
+            for (int kk = 0; kk < kKT / 16; ++kk)
+              mma_ts(d, p + kk * 8, sdesc_at(tv, kk * 2048), kIdescO, (t > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(bar(BAR_O_FULL));
+          mma_commit(bar(BAR_V_EMPTY + b));
         }
-        mma_commit_w(bar(BAR_O_FULL0 + b));
-        mma_commit_w(bar(BAR_V_EMPTY));
+        __syncwarp();
         ++p_it;
         return true;
       };
@@ -270,22 +248,34 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         __syncwarp();
         if (!valid) break;
         if (!(ok = warp_wait_all(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
-        if (nt == 0) mma_commit_w(bar(BAR_Q_EMPTY));
         for (int j = 0; j < nt; ++j) {
           if (j == 0 && !(ok = qk())) break;
           if (j + 1 < nt && !(ok = qk())) break;
-          if (j == (nt > 1 ? nt - 2 : 0))
-            mma_commit_w(bar(BAR_Q_EMPTY));            // the unit's scores are all issued
           if (!(ok = pv())) break;
         }
         if (!ok) break;
         ++unit_count;
       }
       int drain_abort = 0;
-      mma_commit_w(bar(BAR_DRAIN));
+      if (elect_one()) mma_commit(bar(BAR_DRAIN));
+      __syncwarp();
       warp_wait_all(bar(BAR_DRAIN), 0, &drain_abort);
+    } else if (warp == kReadWarps + 1) {
+      // the units' records, up to kRecSlots ahead; the first that is not valid
+      // ends every role
+      for (uint32_t k = 0;; ++k) {
+        const uint32_t slot = k % kRecSlots;
+        if (!warp_wait0(bar(BAR_REC_EMPTY + slot), ((k / kRecSlots) & 1u) ^ 1u, abort_flag)) break;
+        int valid = 0;
+        if (lane == 0) {
+          Unit u;
+          valid = u.valid = decode_unit<kKT>(unit_index(k), prm, u) ? 1 : 0;
+          s_rec[slot] = u;
+          mbar_arrive(bar(BAR_REC_FULL + slot));
+        }
+        if (!__shfl_sync(0xffffffffu, valid, 0)) break;
+      }
     }
-    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft) : "memory");
     // ------------------------------------------------------ softmax / output
@@ -304,14 +294,34 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
       // this thread's row and what it sees; rows that do not exist see all
       const int r = u.r0[0] + trow;
       const bool rvalid = r < prm.rm.RG;
-      // (kept in shared memory: the output and a score row fill the registers)
+      // The query's parts, once the last unit's scores are done with the old ones
+      // (the last of them was waited for).  The span is kept in shared memory:
+      // the output and a score row fill the registers.
       {
         KeySpan sp{0, INT_MAX};
+        const float* q = nullptr;
         if (rvalid) {
           const CacheRow cr = cache_row(prm.a, prm.rm, u.g, r);
           sp = key_span(prm.a, cache_len(prm.a, cr.b), cr.i);
+          q = static_cast<const float*>(prm.a.q) + cr.row * D;
         }
         s_span[trow] = sp;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          float f[16][4];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) get4(q + c + 4 * i, rvalid, f[i]);
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            uint32_t p[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) p[i] = cut2(f[i / 2][i % 2 * 2], f[i / 2][i % 2 * 2 + 1]);
+            tmem_st32(tl + G::kColQ + part * (D / 2) + c / 2, p);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(BAR_Q_FULL));
       }
       const int nt = u.nt;
       float m = -INFINITY, l = 0.f, o[D];
@@ -319,16 +329,17 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
       for (int i = 0; i < D; ++i) o[i] = 0.f;
       // adds tile k's output
       auto add_output = [&](uint32_t k) -> bool {
-        if (!warp_wait_all(bar(BAR_O_FULL0 + (k & 1u)), (k >> 1) & 1u, abort_flag)) return false;
+        if (!warp_wait_all(bar(BAR_O_FULL), k & 1u, abort_flag)) return false;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t t[32];
-          tmem_ld32(tl + kColO + (k & 1u) * D + c * 32, t);
+          tmem_ld32(tl + G::kColO + c * 32, t);
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[c * 32 + i] += __uint_as_float(t[i]);
         }
         tc_fence_before();
+        mbar_arrive(bar(BAR_O_EMPTY));
         return true;
       };
       for (int j = 0; j < nt; ++j, ++it) {
@@ -348,9 +359,9 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
           sees0 = (bits_below(kb) & ~bits_below(ka)) | bits_below(kc);
           sees1 = (bits_below(kb - 32) & ~bits_below(ka - 32)) | bits_below(kc - 32);
         }
-        if (!(ok = warp_wait_all(bar(BAR_S_FULL0 + (it & 1u)), (it >> 1) & 1u, abort_flag))) break;
+        if (!(ok = warp_wait_all(bar(BAR_S_FULL + (it & 1u)), (it >> 1) & 1u, abort_flag))) break;
         tc_fence_after();
-        const uint32_t tS = tl + (it & 1u) * 64, tX = tl + kColX + (it & 1u) * 32;
+        const uint32_t tS = tl + (it & 1u) * 64, tX = tl + G::kColX + (it & 1u) * 32;
         float s[kKT];
         tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(s[0]));
         tmem_ld32(tS + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
@@ -388,7 +399,7 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(BAR_P_FULL0 + (it & 1u)));
+        mbar_arrive(bar(BAR_P_FULL + (it & 1u)));
         if (j > 0 && !(ok = add_output(it - 1))) break;
         if (rescale) {
 #pragma unroll
@@ -422,7 +433,7 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kReadWarps) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
@@ -437,7 +448,7 @@ cudaError_t launch(const UnitParams& prm, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // setmaxnreg.inc waits until the registers it asks for are free, so the split
   // must fit in what the launch allocates
-  if (fa.numRegs != 168) return cudaErrorInvalidConfiguration;
+  if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   fn<<<std::min(prm.units, num_sms()), kThreads, kSmem, s>>>(prm);

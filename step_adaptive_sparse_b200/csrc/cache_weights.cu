@@ -179,18 +179,22 @@ cache_weights_tc_kernel(const __grid_constant__ WMaps tm, const __grid_constant_
         if (!(ok = warp_wait_all(bar(W_Q_FULL + b), ph, abort_flag))) break;
         if (!(ok = warp_wait_all(bar(W_S_EMPTY + b), ph ^ 1u, abort_flag))) break;
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-          mma_ss_w(tmem + b * 128, sdesc_at(dk, off), sdesc_at(dq, b * G::kTileBytes + off),
-                   kIdescQK, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+            mma_ss(tmem + b * 128, sdesc_at(dk, off), sdesc_at(dq, b * G::kTileBytes + off),
+                     kIdescQK, kk > 0);
+          }
+          mma_commit(bar(W_S_FULL + b));
+          mma_commit(bar(W_Q_EMPTY + b));
         }
-        mma_commit_w(bar(W_S_FULL + b));
-        mma_commit_w(bar(W_Q_EMPTY + b));
+        __syncwarp();
         ++it;
       }
       int drain_abort = 0;
-      mma_commit_w(bar(W_DRAIN));
+      if (elect_one()) mma_commit(bar(W_DRAIN));
+      __syncwarp();
       warp_wait_all(bar(W_DRAIN), 0, &drain_abort);
     }
   } else if (warp >= 4) {
@@ -342,21 +346,25 @@ cache_weights_tc32_kernel(const __grid_constant__ WParams p) {
         if (!(ok = warp_wait_all(bar(W_Q_FULL + b), ph, abort_flag))) break;
         if (!(ok = warp_wait_all(bar(W_S_EMPTY + b), ph ^ 1u, abort_flag))) break;
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int x = 0; x < 6; ++x) {
-          const uint32_t ks = part_a(x) * G::kKTerm, qs = (b * 3 + part_b(x)) * G::kQTerm;
+          for (int x = 0; x < 6; ++x) {
+            const uint32_t ks = part_a(x) * G::kKTerm, qs = (b * 3 + part_b(x)) * G::kQTerm;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss_w(tmem + b * kKR32, sdesc_at(dk, ks + (kk >> 2) * G::kKHalf + (kk & 3) * 32),
-                     sdesc_at(dq, qs + (kk >> 2) * G::kQHalf + (kk & 3) * 32), idesc(kKR32, false),
-                     (x > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tmem + b * kKR32, sdesc_at(dk, ks + (kk >> 2) * G::kKHalf + (kk & 3) * 32),
+                       sdesc_at(dq, qs + (kk >> 2) * G::kQHalf + (kk & 3) * 32), idesc(kKR32, false),
+                       (x > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(bar(W_S_FULL + b));
+          mma_commit(bar(W_Q_EMPTY + b));
         }
-        mma_commit_w(bar(W_S_FULL + b));
-        mma_commit_w(bar(W_Q_EMPTY + b));
+        __syncwarp();
         ++it;
       }
       int drain_abort = 0;
-      mma_commit_w(bar(W_DRAIN));
+      if (elect_one()) mma_commit(bar(W_DRAIN));
+      __syncwarp();
       warp_wait_all(bar(W_DRAIN), 0, &drain_abort);
     }
   } else if (warp >= 8) {

@@ -47,5 +47,22 @@ __device__ __forceinline__ void get8(const float* p, bool in, float (&f)[8]) {
   }
 }
 
+// Four values of a row, or zeros, that no other block of the SM will read.
+__device__ __forceinline__ void get4(const float* p, bool in, float (&f)[4]) {
+  f[0] = f[1] = f[2] = f[3] = 0.f;
+  if (in)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+                 : "l"(p));
+}
+// Four values as the operand's 8-byte pieces: part t at t * term.
+__device__ __forceinline__ void put4(uint32_t at, int term, float (&f)[4]) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    const uint32_t x = cut2(f[0], f[1]), y = cut2(f[2], f[3]);
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + t * term), "r"(x), "r"(y) : "memory");
+  }
+}
+
 }  // namespace
 }  // namespace area
