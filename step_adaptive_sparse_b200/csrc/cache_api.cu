@@ -19,25 +19,41 @@ int rows_per_block(int kernel, int dtype, const CacheRows& rm) {
   switch (kernel) {
     case CACHE_TC: return dtype == AREA_DTYPE_BF16 ? 2 * tc_tile_rows(rm) : 128;
     default:
-      if (dtype == AREA_DTYPE_BF16) return rm.RG <= 8 ? 8 : 16;
+      if (dtype == AREA_DTYPE_BF16) return 8;
       return rm.RG <= 2 ? 2 : rm.RG <= 4 ? 4 : 8;
   }
 }
 
-// Splits of the tensor-core kernels' units: those that end first by a model of
-// their time.  128 keys take a unit `tile` us, starting and ending one 4 us, and
-// splits cost the join (5 us, and their outputs written and read again).
-int tc_splits(int64_t units, int64_t keys, int64_t rows, int D, double tile) {
-  const int64_t tiles = cdiv(keys, 128);
-  int best = 1;
-  double least = 0;
-  for (int n = 1; n <= 64 && n <= cdiv(tiles, 2); ++n) {
-    const double t = cdiv(units * n, kSms) * (4.0 + tile * (double)cdiv(tiles, n)) +
-                     (n > 1 ? 5.0 + (double)rows * n * D * 8 / 5.0e6 : 0.0);
-    if (n == 1 || t < least) {
+// What a launch of `units` that need `keys` keys each takes when those are split
+// n ways, in us: waves of `slots` units at once, a unit `fixed` and `per_key` a key.
+// A last wave that is not full goes faster, down to `alone` of that.  Splits
+// cost the join: 3 us, and their outputs written and read again.
+struct SplitCost {
+  int64_t units, keys, slots, rows;
+  int D;
+  double fixed, per_key, alone;
+  double operator()(int64_t n) const {
+    const int64_t all = units * n, waves = all / slots, rest = all % slots;
+    const double k = per_key * (double)cdiv(keys, n);
+    double t = (double)waves * (fixed + k);
+    if (rest) t += fixed + k * std::max(alone, alone + (1 - alone) * (1.5 * rest / slots - 0.5));
+    return n > 1 ? t + 3.0 + (double)rows * n * D * 8 / 5.0e6 : t;
+  }
+};
+// The best of no split and those that fill one to five waves; `most` at most.
+// (More waves even out sequences of different lengths, but each costs.)
+int64_t best_split(const SplitCost& c, int64_t most) {
+  int64_t best = 1;
+  double least = c(1);
+  for (int w = 1; w <= 5; ++w) {
+    const int64_t n = std::min(w * c.slots / c.units, most);
+    if (n <= best) continue;
+    const double t = c(n);
+    if (t < least) {
       least = t;
       best = n;
     }
+    if (n == most) break;
   }
   return best;
 }
@@ -47,26 +63,36 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D) {
   const int RG = l.rows.RG;
   l.used = true;
   l.cluster = 1;
-  l.kernel = RG <= 16 ? CACHE_DEC : CACHE_TC;
+  // Few rows: the tensor-core kernels' 128-row tiles would be nearly empty.  Eight
+  // bf16 rows fill the products' narrow side; nine to 16 are as fast on either
+  // side for short caches and slower here for long ones (64 heads of 8000 keys:
+  // 81 us, there 62).  In fp32 16 rows take 11 us on 2000 keys, there 15, and
+  // 199 on the long ones, there 162; with weights, which there cost a second
+  // pass, 24 rows 148 us for 167, 32 rows 185 for 166.
+  l.kernel = RG <= (dtype == AREA_DTYPE_BF16 ? 8 : op == CACHE_OP_WEIGHTS ? 24 : 16) ? CACHE_DEC
+                                                                                     : CACHE_TC;
   const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, dtype, l.rows));
   int64_t n;
   if (l.kernel == CACHE_TC) {
-    n = tc_splits(blocks, keys, rows, D, dtype == AREA_DTYPE_BF16 ? 1.8 : D / 32.0);
+    // measured per unit: 4 us, and 2.1 us for 128 keys (bf16, 256 rows), 3.2 or
+    // 5.6 us (fp32, 128 rows, D = 64 or 128)
+    const double tile = dtype == AREA_DTYPE_BF16 ? 2.1 : D == 64 ? 3.2 : 5.6;
+    n = best_split({blocks, keys, kSms, rows, D, 4.0, tile / 128, 1.0}, cdiv(keys, 256));
   } else {
-    const int resident = (dtype == AREA_DTYPE_BF16 ? 3 : 2) * (int)kSms;
-    if (blocks * 8 <= resident && (keys <= 4096 || blocks * 8 >= 2 * kSms)) {
+    const int per_sm = dtype == AREA_DTYPE_BF16 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
+    const int64_t slots = per_sm * kSms;
+    if (blocks * 8 <= slots && (keys <= 4096 || blocks * 8 >= 2 * kSms)) {
       // All blocks run at once: a cluster of up to 8 joins its splits itself
-      // (8 sequences' tokens of 500 keys: 6.0 us, with a join launch 7.1).  In
-      // larger grids the blocks of a cluster wait for room together (512 heads
-      // of 4100 keys in 8 splits: 214 us, without clusters 186).
+      // (4 heads of 500 keys: 6.0 us, with a join launch 7.1).  In larger grids
+      // the blocks of a cluster wait for room together (512 heads of 4100 keys in
+      // 8 splits: 214 us, without clusters 186).
       while (l.cluster < 8 && l.cluster * 128 < keys) l.cluster *= 2;
       n = l.cluster;
     } else {
-      // 1024 keys to a split, which starting a block costs little of (the same
-      // heads in 4 splits: 172 us, in 8: 186, in 2: 185), and at most eight
-      // rounds; where that leaves SMs idle, 128 keys
-      n = std::min(cdiv(32 * kSms, blocks), (keys + 512) / 1024);
-      if (blocks * n < 2 * kSms) n = std::min(cdiv(2 * kSms, blocks), cdiv(keys, 128));
+      // all slots together read 6.3 TB/s (64 heads of 8000 keys in 6 splits, 0.86
+      // waves: 51 us, in 8, 1.15 waves: 68)
+      const double key = (dtype == AREA_DTYPE_BF16 ? 4.0 : 8.0) * D * (double)slots / 6.3e6;
+      n = best_split({blocks, keys, slots, rows, D, 3.0, key, 0.64}, cdiv(keys, 128));
     }
   }
   l.nsplit = (int)std::max<int64_t>(n, 1);

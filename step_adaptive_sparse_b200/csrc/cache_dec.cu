@@ -1,7 +1,7 @@
 // Attention over a key/value cache for few query rows (bf16): one pass over
 // the keys, which is what bounds it.
 //
-// A block has up to 8 NT rows of a group and four warps, which take the keys
+// A block has up to 8 rows of a group and four warps, which take the keys
 // 16 at a time in turn.  The products are taken transposed, so that 8 rows
 // fill a whole mma.m16n8k16 and no row is padded beyond that:
 //   S^T (16 keys x 8 rows)    = K (16 x D)    Q^T (D x 8)
@@ -23,6 +23,7 @@
 namespace area {
 namespace {
 
+constexpr int kRows = 8;                     // rows of a block
 constexpr int kStep = 16;                    // keys of a warp and step
 constexpr int kTile = kDecWarps * kStep;        // keys of a block and step
 constexpr float kSlack = 8.f;                // log2 units
@@ -53,10 +54,9 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
   return v;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kDecWarps * 32, (D == 64 ? 5 : 4) - NT)
+template <int D>
+__global__ void __launch_bounds__(kDecWarps * 32, D == 64 ? 4 : 3)
 cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int nrb) {
-  constexpr int kRows = 8 * NT;
   constexpr int kU = D / 32;                 // 16-byte loads of a thread per key row
   constexpr int kG = D / 64;                 // 16-byte loads of a thread per value row
   __shared__ DecSmem<D, kRows> sm;
@@ -118,112 +118,93 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
     load_v(u0);
   }
 
-  // queries: row n of each 8 rows, in the order of the key fragments
-  uint32_t qf[NT][kU][4];
+  // queries: row n, in the order of the key fragments
+  uint32_t qf[kU][4];
+  const int64_t row = sm.row[n];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t row = sm.row[8 * t + n];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (row >= 0)
-        x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * D +
-                                            32 * u + 8 * c);
-      qf[t][u][0] = x.x, qf[t][u][1] = x.y, qf[t][u][2] = x.z, qf[t][u][3] = x.w;
-    }
+  for (int u = 0; u < kU; ++u) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (row >= 0)
+      x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * D +
+                                          32 * u + 8 * c);
+    qf[u][0] = x.x, qf[u][1] = x.y, qf[u][2] = x.z, qf[u][3] = x.w;
   }
-  // a thread's scores are those of rows 2c and 2c + 1 of each 8
-  KeySpan span[NT][2];
-  bool pre[NT][2], all = true;        // all: every row of the block sees the whole list
+  // a thread's scores are those of rows 2c and 2c + 1
+  KeySpan span[2];
+  bool pre[2], all = true;        // all: every row of the block sees the whole list
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = 8 * t + 2 * c + x;
-      span[t][x] = sm.span[r];
-      pre[t][x] = sm.row[r] >= 0 && sees_prefix(a, span[t][x]);
-      if (sm.row[r] >= 0)
-        all = all && (kl.np == 0 || pre[t][x]) &&
-              (kl.total == kl.np ||
-               (span[t][x].hi - kl.lo == kl.total - kl.np - kl.ns && span[t][x].lo == kl.lo));
-    }
+  for (int x = 0; x < 2; ++x) {
+    const int r = 2 * c + x;
+    span[x] = sm.span[r];
+    pre[x] = sm.row[r] >= 0 && sees_prefix(a, span[x]);
+    if (sm.row[r] >= 0)
+      all = all && (kl.np == 0 || pre[x]) &&
+            (kl.total == kl.np ||
+             (span[x].hi - kl.lo == kl.total - kl.np - kl.ns && span[x].lo == kl.lo));
+  }
   all = __all_sync(0xffffffffu, all);
 
-  float o[NT][kG * 4][4], m[NT][2], l[NT][2];
+  float o[kG * 4][4], m[2], l[2];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
+  for (int i = 0; i < kG * 4; ++i)
 #pragma unroll
-    for (int i = 0; i < kG * 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
-    m[t][0] = m[t][1] = -INFINITY;
-    l[t][0] = l[t][1] = 0.f;
-  }
+    for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+  m[0] = m[1] = -INFINITY;
+  l[0] = l[1] = 0.f;
 
   for (; u0 < uend; u0 += kTile) {
-    float s[NT][4];
+    float s[4] = {};
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        mma_bf16(s[t], kf[0][u].x, kf[1][u].x, kf[0][u].y, kf[1][u].y, qf[t][u][0], qf[t][u][1]);
-        mma_bf16(s[t], kf[0][u].z, kf[1][u].z, kf[0][u].w, kf[1][u].w, qf[t][u][2], qf[t][u][3]);
-      }
+    for (int u = 0; u < kU; ++u) {
+      mma_bf16(s, kf[0][u].x, kf[1][u].x, kf[0][u].y, kf[1][u].y, qf[u][0], qf[u][1]);
+      mma_bf16(s, kf[0][u].z, kf[1][u].z, kf[0][u].w, kf[1][u].w, qf[u][2], qf[u][3]);
     }
     if (u0 + kTile < uend) load_k(u0 + kTile);
-    // s[t][0..3]: key n of rows 2c, 2c + 1, then key n + 8
+    // s[0..3]: key n of rows 2c, 2c + 1, then key n + 8
     const bool whole = all && u0 + kStep <= uend;
     bool grow = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        s[t][x] *= a.scale_log2;
-        if (!whole || out.logits) {
-          const int u = u0 + n + 8 * (x >> 1), w = u - kl.np;
-          const int key = w < kl.ns ? w : kl.lo + (w - kl.ns);
-          const bool in = u < uend && (u < kl.np ? pre[t][x & 1] : sees_own(a, span[t][x & 1], key));
-          if (out.logits && in) {
-            const int64_t row = sm.row[8 * t + 2 * c + (x & 1)];
-            if (row >= 0) out.logits[row * a.S + key] = s[t][x];
-          }
-          if (!in) s[t][x] = -INFINITY;
+    for (int x = 0; x < 4; ++x) {
+      s[x] *= a.scale_log2;
+      if (!whole || out.logits) {
+        const int u = u0 + n + 8 * (x >> 1), w = u - kl.np;
+        const int key = w < kl.ns ? w : kl.lo + (w - kl.ns);
+        const bool in = u < uend && (u < kl.np ? pre[x & 1] : sees_own(a, span[x & 1], key));
+        if (out.logits && in) {
+          const int64_t row = sm.row[2 * c + (x & 1)];
+          if (row >= 0) out.logits[row * a.S + key] = s[x];
         }
-        grow = grow || s[t][x] > m[t][x & 1] + kSlack;
+        if (!in) s[x] = -INFINITY;
       }
+      grow = grow || s[x] > m[x & 1] + kSlack;
+    }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int x = 0; x < 2; ++x) {
+        float mx = fmaxf(s[x], s[x + 2]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float mx = fmaxf(s[t][x], s[t][x + 2]);
+        for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+        const float mn = fmaxf(m[x], mx);
+        const float alpha = ex2(m[x] - (mn == -INFINITY ? 0.f : mn));
+        m[x] = mn;
+        l[x] *= alpha;
 #pragma unroll
-          for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
-          const float mn = fmaxf(m[t][x], mx);
-          const float alpha = ex2(m[t][x] - (mn == -INFINITY ? 0.f : mn));
-          m[t][x] = mn;
-          l[t][x] *= alpha;
-#pragma unroll
-          for (int i = 0; i < kG * 4; ++i) {
-            o[t][i][x] *= alpha;
-            o[t][i][x + 2] *= alpha;
-          }
+        for (int i = 0; i < kG * 4; ++i) {
+          o[i][x] *= alpha;
+          o[i][x + 2] *= alpha;
         }
-    }
-    uint32_t pf[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        // nothing seen so far: every weight is 0
-        const float ref = m[t][x & 1] == -INFINITY ? 0.f : m[t][x & 1];
-        s[t][x] = ex2(s[t][x] - ref);
-        l[t][x & 1] += s[t][x];
       }
-      pf[t][0] = transpose8x8(pack2(s[t][0], s[t][1]));
-      pf[t][1] = transpose8x8(pack2(s[t][2], s[t][3]));
     }
+    uint32_t pf[2];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      // nothing seen so far: every weight is 0
+      const float ref = m[x & 1] == -INFINITY ? 0.f : m[x & 1];
+      s[x] = ex2(s[x] - ref);
+      l[x & 1] += s[x];
+    }
+    pf[0] = transpose8x8(pack2(s[0], s[1]));
+    pf[1] = transpose8x8(pack2(s[2], s[3]));
 #pragma unroll
     for (int q = 0; q < kG; ++q) {
       const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&vf[0][q]);
@@ -234,8 +215,7 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
       for (int w = 0; w < 4; ++w) {
         const uint32_t a0 = __byte_perm(w0[w], w1[w], 0x5410), a1 = __byte_perm(w0[w], w1[w], 0x7632);
         const uint32_t a2 = __byte_perm(w2[w], w3[w], 0x5410), a3 = __byte_perm(w2[w], w3[w], 0x7632);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma_bf16(o[t][q * 4 + w], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+        mma_bf16(o[q * 4 + w], a0, a1, a2, a3, pf[0], pf[1]);
       }
     }
     if (u0 + kTile < uend) load_v(u0 + kTile);
@@ -243,37 +223,34 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
 
   // the warps' results: rows 2c, 2c + 1 and dims 64 q + 8 n + 2 w, + 1
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int x = 0; x < 2; ++x) {
+    const int r = 2 * c + x;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = 8 * t + 2 * c + x;
-#pragma unroll
-      for (int y = 4; y < 32; y <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], y);
-      if (n == 0) {
-        sm.m[warp][r] = m[t][x];
-        sm.l[warp][r] = l[t][x];
-      }
-#pragma unroll
-      for (int i = 0; i < kG * 4; ++i)
-        *reinterpret_cast<float2*>(&sm.o[warp][r][64 * (i >> 2) + 8 * n + 2 * (i & 3)]) =
-            make_float2(o[t][i][x], o[t][i][x + 2]);
+    for (int y = 4; y < 32; y <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], y);
+    if (n == 0) {
+      sm.m[warp][r] = m[x];
+      sm.l[warp][r] = l[x];
     }
+#pragma unroll
+    for (int i = 0; i < kG * 4; ++i)
+      *reinterpret_cast<float2*>(&sm.o[warp][r][64 * (i >> 2) + 8 * n + 2 * (i & 3)]) =
+          make_float2(o[i][x], o[i][x + 2]);
+  }
   dec_finish<__nv_bfloat16>(sm, a, out, sp, kvh, t0 * kTile, uend);
 }
 
-template <int D, int NT>
+template <int D>
 cudaError_t launch(const CacheArgs& a, const CacheRows& rm, const CacheOut& out, cudaStream_t s) {
-  const int nrb = (rm.RG + 8 * NT - 1) / (8 * NT);
+  const int nrb = (rm.RG + kRows - 1) / kRows;
   const int64_t grid = (int64_t)rm.groups * nrb * out.nsplit;
-  return launch_dec(cache_dec_kernel<D, NT>, grid, a, rm, out, nrb, s);
+  return launch_dec(cache_dec_kernel<D>, grid, a, rm, out, nrb, s);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_dec_bf16(const CacheArgs& a, const CacheRows& rm, const CacheOut& out,
                                   cudaStream_t s) {
-  if (rm.RG <= 8) return a.D == 64 ? launch<64, 1>(a, rm, out, s) : launch<128, 1>(a, rm, out, s);
-  return a.D == 64 ? launch<64, 2>(a, rm, out, s) : launch<128, 2>(a, rm, out, s);
+  return a.D == 64 ? launch<64>(a, rm, out, s) : launch<128>(a, rm, out, s);
 }
 
 }  // namespace area

@@ -5,45 +5,87 @@
 namespace area {
 namespace {
 
-// One block of four warps per row.  The row's output is
-//   sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s,   m = max_s m_s;
-// the warps take the slots in turn and add up in shared memory in a fixed
-// order.  A slot without a key has l = 0 and its output is not read.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) cache_join_kernel(const float* __restrict__ part_o,
-                                                         const float2* __restrict__ part_ml,
-                                                         int slots, int64_t rows, T* o,
-                                                         float* lse) {
-  constexpr int kPer = D / 32;
-  __shared__ float s_o[4][D], s_l[4];
-  const int64_t row = blockIdx.x;
+// The row's output is
+//   sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s,   m = max_s m_s.
+// Many rows of few slots: a warp to a row; otherwise a block, whose warps take the
+// slots in turn and add up in shared memory in a fixed order (1024 rows of 8
+// slots: 6 us, with a warp to a row 11).  Four slots are loaded at once.  A slot without a key has l = 0
+// and its output, which nobody wrote, counts as zeros.
+constexpr int kJoinWarps = 8;
+template <typename T, int D, bool BLOCK>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+cache_join_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml, int slots,
+                  int64_t rows, T* o, float* lse) {
+  constexpr int kPer = D / 32;                             // columns of a lane
+  __shared__ float s_o[BLOCK ? kJoinWarps : 1][D], s_l[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kJoinWarps + warp;
+  if (row >= rows) return;                                 // !BLOCK: whole warps
   float m = -INFINITY;
   for (int s = lane; s < slots; s += 32) m = fmaxf(m, part_ml[s * rows + row].x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float ref = m == -INFINITY ? 0.f : m;
   float acc[kPer] = {}, l = 0.f;
-  for (int s = warp; s < slots; s += 4) {
-    const float2 ml = part_ml[s * rows + row];
-    if (ml.y == 0.f) continue;
-    const float w = exp2f(ml.x - ref);
-    l += w * ml.y;
-    const float* src = part_o + (s * rows + row) * D + lane * kPer;
+  constexpr int kStep = BLOCK ? kJoinWarps : 1;
+  for (int s0 = BLOCK ? warp : 0; s0 < slots; s0 += 4 * kStep) {
+    float x[4][kPer];
+    float2 ml[4];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = fmaf(w, src[i], acc[i]);
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i * kStep;
+      ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[i][j] = 0.f;
+      if (s >= slots) continue;
+      ml[i] = part_ml[s * rows + row];
+      const float* src = part_o + (s * rows + row) * D + lane * kPer;
+      if constexpr (kPer == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        x[i][0] = f.x, x[i][1] = f.y, x[i][2] = f.z, x[i][3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        x[i][0] = f.x, x[i][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool any = ml[i].y != 0.f;
+      const float w = any ? exp2f(ml[i].x - ref) : 0.f;
+      l = fmaf(w, ml[i].y, l);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) acc[j] = fmaf(w, any ? x[i][j] : 0.f, acc[j]);
+    }
   }
+  if constexpr (BLOCK) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = acc[i];
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  const float total = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-  for (int d = threadIdx.x; d < D; d += 128) {
-    const float v = (s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d]);
-    store_from_float(o, row * D + d, total == 0.f ? 0.f : v / total);
+    for (int j = 0; j < kPer; ++j) s_o[warp][lane * kPer + j] = acc[j];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp > 0) return;
+    l = s_l[0];
+    for (int w = 1; w < kJoinWarps; ++w) {
+      l += s_l[w];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) acc[j] += s_o[w][lane * kPer + j];
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) acc[j] = l == 0.f ? 0.f : acc[j] * inv;
+  T* dst = o + row * D + lane * kPer;
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (kPer == 4)
+      *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    else
+      *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + j) = __floats2bfloat162_rn(acc[j], acc[j + 1]);
   }
   // a row without a weight: +inf, so that 2^(x - lse) is 0 for every key
-  if (lse && threadIdx.x == 0) lse[row] = total == 0.f ? INFINITY : ref + log2f(total);
+  if (lse && lane == 0) lse[row] = l == 0.f ? INFINITY : ref + log2f(l);
 }
 
 // kWKeys keys of a key head to a thread, a block apart; a key's rows' weights
@@ -83,20 +125,24 @@ __global__ void __launch_bounds__(kWThreads) cache_weights_kernel(const CacheArg
   }
 }
 
+template <typename T>
+void join(const CacheArgs& a, const float* part_o, const float2* part_ml, int slots, int64_t rows,
+          float* lse, cudaStream_t s) {
+  T* o = static_cast<T*>(a.o);
+  const int threads = kJoinWarps * 32;
+  const bool block = slots > 16 || rows <= 8192;
+  const unsigned grid = (unsigned)(block ? rows : (rows + kJoinWarps - 1) / kJoinWarps);
+  auto fn = a.D == 64 ? (block ? cache_join_kernel<T, 64, true> : cache_join_kernel<T, 64, false>)
+                      : (block ? cache_join_kernel<T, 128, true> : cache_join_kernel<T, 128, false>);
+  fn<<<grid, threads, 0, s>>>(part_o, part_ml, slots, rows, o, lse);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const float2* part_ml,
                               int slots, int64_t rows, float* lse, int dtype, cudaStream_t s) {
-  const unsigned grid = (unsigned)rows;
-  if (dtype == AREA_DTYPE_F32) {
-    float* o = static_cast<float*>(a.o);
-    if (a.D == 64) cache_join_kernel<float, 64><<<grid, 128, 0, s>>>(part_o, part_ml, slots, rows, o, lse);
-    else cache_join_kernel<float, 128><<<grid, 128, 0, s>>>(part_o, part_ml, slots, rows, o, lse);
-  } else {
-    auto* o = static_cast<__nv_bfloat16*>(a.o);
-    if (a.D == 64) cache_join_kernel<__nv_bfloat16, 64><<<grid, 128, 0, s>>>(part_o, part_ml, slots, rows, o, lse);
-    else cache_join_kernel<__nv_bfloat16, 128><<<grid, 128, 0, s>>>(part_o, part_ml, slots, rows, o, lse);
-  }
+  if (dtype == AREA_DTYPE_F32) join<float>(a, part_o, part_ml, slots, rows, lse, s);
+  else join<__nv_bfloat16>(a, part_o, part_ml, slots, rows, lse, s);
   return cudaGetLastError();
 }
 
