@@ -155,7 +155,7 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   if (p->rows > (int64_t(1) << 58) / (S + 1)) return AREA_EUNSUPPORTED;
   p->bytes = p->off_logits + (weights && few ? ceil256(p->rows * S * 4) : 0);
   const int64_t blocks = cdiv(m.rows.RG, 8) * m.rows.groups * std::max(m.nsplit, 1);
-  if (blocks > INT_MAX || cdiv(S, 256) * B * Hk > INT_MAX) return AREA_EUNSUPPORTED;
+  if (blocks > INT_MAX || cdiv(S, 128) * B * Hk > INT_MAX) return AREA_EUNSUPPORTED;
   return AREA_OK;
 }
 

@@ -470,7 +470,7 @@ cudaError_t launch_cache_tc32(const CacheArgs& a, const CacheRows& rm, const Cac
                               cudaStream_t s) {
   UnitParams p{a, rm, out, (rm.RG + 127) / 128, 128, 1, 0, 0};
   p.units = (int)((int64_t)rm.groups * p.nrb * out.nsplit);
-  p.heavy_first = a.causal && !rm.pool_rows && a.window >= a.S;
+  p.heavy_first = a.causal && !rm.pool_rows;
   return a.D == 64 ? launch<64>(p, s) : launch<128>(p, s);
 }
 
