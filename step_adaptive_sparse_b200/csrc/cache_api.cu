@@ -296,8 +296,8 @@ int area_cache_evict(const void* k, const void* v, const float* acc, const int* 
   if (D != 64 && D != 128) return AREA_EUNSUPPORTED;
   if (S > INT_MAX - 4096 || So > INT_MAX - 4096) return AREA_EUNSUPPORTED;   // 32-bit indexes
   const int64_t heads = (int64_t)B * Hk, elem = dtype == AREA_DTYPE_F32 ? 4 : 2;
-  if (heads > INT_MAX || heads * (2 * D * elem / 64 + 1) > INT_MAX ||
-      heads * area::cdiv(budget, 64) > INT_MAX)
+  if (heads > INT_MAX || heads * std::max<int64_t>(2 * D * elem / 64 + 1, 8) > INT_MAX ||
+      heads * area::cdiv(budget, 512 / (D * elem / 16)) > INT_MAX)
     return AREA_EUNSUPPORTED;                                                // grid sizes
   for (const void* p : {k, v, (const void*)ko, (const void*)vo})
     if (!aligned(p, 16)) return AREA_EINVAL;

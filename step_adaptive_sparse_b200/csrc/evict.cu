@@ -3,15 +3,16 @@
 // Of a sequence of n > budget tokens each key head keeps the first `sinks`,
 // the last `recent` and, of the tokens between, the budget - sinks - recent
 // with the largest accumulated weight (ties: the lowest index), in their
-// order.  Two launches: the choice, which leaves the kept tokens' indexes, and
-// the copy of their rows.
+// order.  One launch chooses and copies; in place the rows move in a second.
+#include <cooperative_groups.h>
+
 #include "cache.cuh"
 
 namespace area {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kPer = 4, kTile = kThreads * kPer;     // candidates of a thread, of a block's step
 
 // An integer that orders as the weight does; -0 as 0, a NaN as -infinity.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -27,46 +28,119 @@ __device__ __forceinline__ int evict_len(const EvictArgs& e, int b) {
   return n < 0 ? 0 : n > e.S ? e.S : n;
 }
 
-// One block per (sequence, key head).  Radix selection of the smallest kept
-// key from the top byte down, then one ordered pass that writes the indexes.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs e) {
-  __shared__ int s_hist[256];
-  __shared__ int s_bin, s_above;
-  __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
-  const int g = blockIdx.x, b = g / e.Hk;
+// A thread's share of a block's copy: rows i0, i0 + step, ... < n of K and V, 16
+// bytes of each per load, two rows in flight.  from(i): row i's old and new place.
+template <typename F>
+__device__ __forceinline__ void copy_rows(const EvictArgs& e, int64_t g, int n, F from) {
+  const int chunks = e.D * e.elem / 16;                  // 16-byte pieces of a row: 8, 16 or 32
+  const int per = kThreads / chunks, c = threadIdx.x % chunks;
+  const uint4 *k = static_cast<const uint4*>(e.k) + g * e.S * chunks + c;
+  const uint4 *v = static_cast<const uint4*>(e.v) + g * e.S * chunks + c;
+  uint4 *ko = static_cast<uint4*>(e.ko) + g * e.So * chunks + c;
+  uint4 *vo = static_cast<uint4*>(e.vo) + g * e.So * chunks + c;
+  for (int i = threadIdx.x / chunks; i < n; i += 2 * per) {
+    const int2 a = from(i), b = from(min(i + per, n - 1));
+    const uint4 ka = __ldcs(k + (int64_t)a.x * chunks), va = __ldcs(v + (int64_t)a.x * chunks);
+    const uint4 kb = __ldcs(k + (int64_t)b.x * chunks), vb = __ldcs(v + (int64_t)b.x * chunks);
+    __stcs(ko + (int64_t)a.y * chunks, ka);
+    __stcs(vo + (int64_t)a.y * chunks, va);
+    if (i + per < n) {
+      __stcs(ko + (int64_t)b.y * chunks, kb);
+      __stcs(vo + (int64_t)b.y * chunks, vb);
+    }
+  }
+}
+
+// A cluster per (sequence, key head), each block a contiguous share of the
+// candidates.  Radix selection of the smallest kept key from the top byte down:
+// a block counts its share, the counts are added up over the cluster's shared
+// memory; the lower ranks' counts also give a block the place of its first kept
+// token.  Then every block writes its share's indexes in order and, with COPY,
+// copies their rows.  Counts are integers: their order does not matter.  Without COPY,
+// which serves long caches, candidates stay in registers over the passes (256 heads of
+// 8192 tokens: 3 us less; caches of one step lose 1.5 us to the longer code).
+template <bool COPY>
+__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs e, int cs) {
+  __shared__ int s_hist[4][256];
+  __shared__ int s_tot[256];
+  __shared__ int s_bin, s_above, s_gt, s_eq;   // kept keys above the threshold, equal to it, in lower ranks
+  __shared__ int s_wgt[kWarps], s_weq[kWarps];
+  __shared__ int s_list[kTile];
+  const auto cluster = cooperative_groups::this_cluster();
+  const int64_t g = blockIdx.x / cs;
+  const int rank = blockIdx.x % cs, b = (int)(g / e.Hk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = evict_len(e, b);
-  int* idx = e.idx + (int64_t)g * e.So;
   const int kept = min(n, e.budget);
-  if (g % e.Hk == 0 && tid == 0) e.lenso[b] = kept;
-  for (int j = kept + tid; j < e.So; j += kSelThreads) idx[j] = -1;
-  if (n <= e.budget) {
-    for (int j = tid; j < n; j += kSelThreads) idx[j] = j;
-    return;
+  const float* acc = e.acc + g * e.S;
+  int* idx = e.idx + g * e.So;
+  float* acco = e.acco + g * e.So;
+  auto share = [&](int of, int r) { return (int)((int64_t)of * r / cs); };
+  if (g % e.Hk == 0 && rank == 0 && tid == 0) e.lenso[b] = kept;
+  for (int j = kept + share(e.So - kept, rank) + tid; j < kept + share(e.So - kept, rank + 1);
+       j += kThreads) {
+    idx[j] = -1;
+    if (COPY) acco[j] = 0.f;
   }
-  const float* acc = e.acc + (int64_t)g * e.S + e.sinks;
-  const int cand = n - e.sinks - e.recent;               // tokens to choose from
-  const int want = e.budget - e.sinks - e.recent;        // < cand
-  for (int j = tid; j < e.sinks; j += kSelThreads) idx[j] = j;
-  for (int j = tid; j < e.recent; j += kSelThreads) idx[e.sinks + want + j] = n - e.recent + j;
-  if (want == 0) return;
+  // what is kept in any case: all, or the sinks and the last tokens
+  const bool all = n <= e.budget;
+  const int want = all ? 0 : e.budget - e.sinks - e.recent;      // to be chosen
+  const int first = all ? n : e.sinks, fixed = all ? n : e.sinks + e.recent;
+  const int f0 = share(fixed, rank), nf = share(fixed, rank + 1) - f0;
+  auto always = [&](int i) {
+    const int f = f0 + i;
+    return f < first ? make_int2(f, f) : make_int2(n - fixed + f, want + f);
+  };
+  for (int i = tid; i < nf; i += kThreads) {
+    const int2 m = always(i);
+    idx[m.y] = m.x;
+    if (COPY) acco[m.y] = acc[m.x];
+  }
+  if (COPY) copy_rows(e, g, nf, always);
+  if (want == 0) return;                                 // the whole cluster does
 
+  acc += e.sinks;
+  const int cand = n - e.sinks - e.recent;               // tokens to choose from, > want
+  const int c0 = share(cand, rank), c1 = share(cand, rank + 1);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) s_hist[p][tid] = 0;
+  if (tid == 0) s_gt = s_eq = 0;
+  __syncthreads();
+  constexpr int kHeld = COPY ? 0 : 16;                   // steps of kThreads
+  uint32_t held[kHeld + 1];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int j = c0 + tid + i * kThreads;
+    held[i] = j < c1 ? weight_key(acc[j]) : 0;
+  }
   uint32_t prefix = 0;           // the bytes of the threshold found so far
   int left = want;               // kept keys among those that share them
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) s_hist[i] = 0;
-    __syncthreads();
-    for (int j = tid; j < cand; j += kSelThreads) {
-      const uint32_t key = weight_key(acc[j]);
-      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&s_hist[key >> shift & 255], 1);
+#pragma unroll 1
+  for (int p = 0; p < 4; ++p) {
+    const int shift = 24 - 8 * p;
+    auto count = [&](uint32_t key) {
+      if (p == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
+        atomicAdd(&s_hist[p][key >> shift & 255], 1);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (c0 + tid + i * kThreads < c1) count(held[i]);
+#pragma unroll 4
+    for (int j = c0 + kHeld * kThreads + tid; j < c1; j += kThreads) count(weight_key(acc[j]));
+    cluster.sync();
+    int total = 0, lower = 0;                            // of bin tid
+    for (int r = 0; r < cs; ++r) {
+      const int x = *cluster.map_shared_rank(&s_hist[p][tid], r);
+      total += x;
+      if (r < rank) lower += x;
     }
+    s_tot[tid] = total;
     __syncthreads();
     if (warp == 0) {
-      // lane 0 holds the eight highest bins; `before` = keys in higher lanes' bins
+      // lane 0 holds the eight highest bins; `above` = keys in higher bins
       int h[8], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += h[i] = s_hist[255 - (lane * 8 + i)];
+      for (int i = 0; i < 8; ++i) sum += h[i] = s_tot[255 - (lane * 8 + i)];
       int incl = sum;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
@@ -86,61 +160,79 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       }
     }
     __syncthreads();
+    if (tid > s_bin && lower) atomicAdd(&s_gt, lower);
+    if (p == 3 && tid == s_bin) s_eq = lower;
     prefix |= (uint32_t)s_bin << shift;
     left -= s_above;
     __syncthreads();
   }
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   // keys above the threshold are kept, and the first `left` of those equal to it
-  int gt0 = 0, eq0 = 0;          // found in earlier tiles
-  for (int j0 = 0; j0 < cand; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t key = j < cand ? weight_key(acc[j]) : 0;
-    const unsigned gt = __ballot_sync(0xffffffffu, j < cand && key > prefix);
-    const unsigned eq = __ballot_sync(0xffffffffu, j < cand && key == prefix);
-    if (lane == 0) {
-      s_gt[warp] = __popc(gt);
-      s_eq[warp] = __popc(eq);
+  int gt0 = s_gt, eq0 = s_eq;    // found so far
+  for (int j0 = c0; j0 < c1; j0 += kTile) {
+    const int j = j0 + tid * kPer;
+    float w[kPer];
+    uint32_t gt = 0, eq = 0;     // one bit per candidate of the thread
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      w[i] = j + i < c1 ? acc[j + i] : 0.f;
+      const uint32_t key = weight_key(w[i]);
+      if (j + i < c1 && key > prefix) gt |= 1u << i;
+      if (j + i < c1 && key == prefix) eq |= 1u << i;
     }
+    int igt = __popc(gt), ieq = __popc(eq);              // including this thread's
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int tg = __shfl_up_sync(0xffffffffu, igt, x), te = __shfl_up_sync(0xffffffffu, ieq, x);
+      if (lane >= x) igt += tg, ieq += te;
+    }
+    if (lane == 31) s_wgt[warp] = igt, s_weq[warp] = ieq;
     __syncthreads();
-    int gtb = gt0, eqb = eq0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      const int x = s_gt[w], y = s_eq[w];
-      if (w < warp) {
-        gtb += x;
-        eqb += y;
+    const int start = gt0 + min(eq0, left);              // kept tokens before this step
+    int gtb = gt0 + igt - __popc(gt), eqb = eq0 + ieq - __popc(eq);
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+      const int tg = s_wgt[x], te = s_weq[x];
+      if (x < warp) gtb += tg, eqb += te;
+      gt0 += tg, eq0 += te;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if ((gt >> i & 1u) || ((eq >> i & 1u) && eqb < left)) {
+        const int at = gtb + min(eqb, left);
+        idx[e.sinks + at] = e.sinks + j + i;
+        if (COPY) {
+          acco[e.sinks + at] = w[i];
+          s_list[at - start] = e.sinks + j + i;
+        }
       }
-      gt0 += x;
-      eq0 += y;
+      gtb += gt >> i & 1u, eqb += eq >> i & 1u;
     }
-    const unsigned below = (1u << lane) - 1;
-    gtb += __popc(gt & below);
-    eqb += __popc(eq & below);
-    const bool mine_eq = eq >> lane & 1;
-    if ((gt >> lane & 1) || (mine_eq && eqb < left))
-      idx[e.sinks + gtb + min(eqb, left)] = e.sinks + j;
     __syncthreads();
+    if (COPY) {
+      copy_rows(e, g, gt0 + min(eq0, left) - start,
+                [&](int i) { return make_int2(s_list[i], e.sinks + start + i); });
+      __syncthreads();
+    }
   }
+  // the others have read this block's counts
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Copies the kept rows: 16 bytes of K and of V per thread and step.
-__global__ void __launch_bounds__(256) evict_copy_kernel(const EvictArgs e, int blocks_per_head) {
-  const int g = blockIdx.x / blocks_per_head, blk = blockIdx.x % blocks_per_head;
-  const int m = min(evict_len(e, g / e.Hk), e.budget);
-  const int* idx = e.idx + (int64_t)g * e.So;
-  const int chunks = e.D * e.elem / 16;                  // 16-byte pieces of a row
-  const int64_t src0 = (int64_t)g * e.S * chunks, dst0 = (int64_t)g * e.So * chunks;
-  const uint4 *k = static_cast<const uint4*>(e.k), *v = static_cast<const uint4*>(e.v);
-  uint4 *ko = static_cast<uint4*>(e.ko), *vo = static_cast<uint4*>(e.vo);
-  const int per = 256 / chunks;                          // rows of a step
-  const int c = threadIdx.x % chunks;
-  for (int j = blk * per + threadIdx.x / chunks; j < m; j += blocks_per_head * per) {
-    const int64_t src = src0 + (int64_t)idx[j] * chunks + c, dst = dst0 + (int64_t)j * chunks + c;
-    const uint4 x = k[src], y = v[src];
-    ko[dst] = x;
-    vo[dst] = y;
-  }
-  for (int j = blk * 256 + threadIdx.x; j < e.So; j += blocks_per_head * 256)
-    e.acco[(int64_t)g * e.So + j] = j < m ? e.acc[(int64_t)g * e.S + idx[j]] : 0.f;
+// The copy of the kept rows on its own: blocks_per_head blocks take the rows of a
+// head in equal shares, two to a thread (256 heads of 8192 tokens to 4096: 160 us, all
+// of copy bandwidth).
+__global__ void __launch_bounds__(kThreads) evict_copy_kernel(const EvictArgs e,
+                                                              int blocks_per_head) {
+  const int64_t g = blockIdx.x / blocks_per_head;
+  const int blk = blockIdx.x % blocks_per_head;
+  const int m = min(evict_len(e, (int)(g / e.Hk)), e.budget);
+  const int* idx = e.idx + g * e.So;
+  const int r0 = (int)((int64_t)m * blk / blocks_per_head);
+  const int r1 = (int)((int64_t)m * (blk + 1) / blocks_per_head);
+  copy_rows(e, g, r1 - r0, [&](int i) { return make_int2(idx[r0 + i], r0 + i); });
+  for (int j = blk * kThreads + threadIdx.x; j < e.So; j += blocks_per_head * kThreads)
+    e.acco[g * e.So + j] = j < m ? e.acc[g * e.S + idx[j]] : 0.f;
 }
 
 // The copy within the cache itself.  A kept row moves to an index not above
@@ -194,21 +286,43 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs e, int 
   }
 }
 
+// Blocks of a cluster: a share of `least` candidates at least, and four blocks to an
+// SM at most (256 heads of 8192 tokens: 2 blocks 183 us, 8 blocks 217; 8 heads of
+// 40000: 8 blocks 31 us, 2 blocks 56; 2048 heads of 500: one block 73, 2 blocks 100).
+int evict_cluster(int heads, int S, int least, int most) {
+  int cs = 1;
+  while (cs < most && S > least * cs && (int64_t)heads * cs * 2 <= 4 * 148) cs *= 2;
+  return cs;
+}
+
 }  // namespace
 
 cudaError_t launch_cache_evict(const EvictArgs& e, cudaStream_t s) {
+  // Short caches: the blocks that choose also copy (2 heads of 600 tokens: 9.1 us, with
+  // a launch for the copy 11.6; 2048 heads of 500: 73 and 80).  Long ones: more blocks
+  // copy than choose (8 heads of 40000: 31 us, in one launch 51; 256 of 8192: 183, 196).
   const int heads = e.B * e.Hk;
-  evict_select_kernel<<<(unsigned)heads, kSelThreads, 0, s>>>(e);
-  cudaError_t st = cudaGetLastError();
+  const bool in_place = e.k == e.ko, one = !in_place && e.S <= kTile;
+  const int cs = one ? evict_cluster(heads, e.S, 256, 4) : evict_cluster(heads, e.S, 1024, 8);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(heads * cs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t st = cudaLaunchKernelEx(&cfg, one ? evict_kernel<true> : evict_kernel<false>, e, cs);
   if (st != cudaSuccess) return st;
-  const int chunks = e.D * e.elem / 16;
-  if (e.k == e.ko) {
-    const int cols = chunks / 4;
+  if (in_place) {
+    const int cols = e.D * e.elem / 64;
     evict_move_kernel<<<(unsigned)(heads * (2 * cols + 1)), 256, 0, s>>>(e, cols);
-  } else {
-    const int per = 256 / chunks * 8;                    // rows of a block: eight steps
+  } else if (!one) {
+    const int per = kThreads / (e.D * e.elem / 16) * 2;  // rows of a block: two of each thread
     const int nb = (e.budget + per - 1) / per;
-    evict_copy_kernel<<<(unsigned)((int64_t)heads * nb), 256, 0, s>>>(e, nb);
+    evict_copy_kernel<<<(unsigned)((int64_t)heads * nb), kThreads, 0, s>>>(e, nb);
   }
   return cudaGetLastError();
 }
