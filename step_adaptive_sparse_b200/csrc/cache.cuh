@@ -43,6 +43,7 @@ struct CacheRows {
   int pool_rows;   // 0: not pooled
   int use_prefix;  // the launch covers the prefix keys
   int use_own;     // the launch covers the sequences' own keys
+  int by_length;   // kernels for few rows: the longest sequences' blocks first
 };
 
 // Where a launch leaves its results.
@@ -182,10 +183,11 @@ cudaError_t launch_cache_dec_f32(const CacheArgs& a, const CacheRows& rm, const 
 // lse when that is given.
 cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const float2* part_ml,
                               int slots, int64_t rows, float* lse, int dtype, cudaStream_t s);
+// The same for the kernels for few rows when they have left scores, and then
 // acco[b, hk, j] = acc[b, hk, j] + sum over the rows that see j of
-// 2^(logits[row][j] - lse[row]).
-cudaError_t launch_cache_weights(const CacheArgs& a, const float* logits, const float* lse,
-                                 const float* acc, float* acco, cudaStream_t s);
+// 2^(logits[row][j] - log2-sum of the row).
+cudaError_t launch_cache_join_weights(const CacheArgs& a, const CacheOut& out, int slots, int dtype,
+                                      cudaStream_t s);
 
 // Rows of a row tile of the bf16 tensor-core kernel: 128, or in a pooled launch as
 // many whole sequences' rows as fit.
@@ -198,8 +200,8 @@ cudaError_t launch_cache_tc32(const CacheArgs& a, const CacheRows& rm, const Cac
                               cudaStream_t s);
 cudaError_t read_and_clear_cache_tc_error(int* code);
 cudaError_t read_and_clear_cache_tc32_error(int* code);
-// The same sums as launch_cache_weights for many rows of a key head: the scores
-// are computed once more instead of read.
+// The same sums for many rows of a key head: the scores are computed once more
+// instead of read.
 cudaError_t launch_cache_weights_tc(const CacheArgs& a, const float* lse, const float* acc,
                                     float* acco, int dtype, cudaStream_t s);
 cudaError_t read_and_clear_cache_weights_error(int* code);

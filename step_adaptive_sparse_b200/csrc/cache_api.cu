@@ -58,8 +58,9 @@ int64_t best_split(const SplitCost& c, int64_t most) {
   return best;
 }
 
-// Chooses a launch's kernel, and splits its keys (at most `keys` of them).
-void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D) {
+// Chooses a launch's kernel, and splits its keys (at most `keys` of them; even: most
+// sequences have as many).
+void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D, bool even) {
   const int RG = l.rows.RG;
   l.used = true;
   l.cluster = 1;
@@ -93,6 +94,10 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D) {
       // waves: 51 us, in 8, 1.15 waves: 68)
       const double key = (dtype == AREA_DTYPE_BF16 ? 4.0 : 8.0) * D * (double)slots / 6.3e6;
       n = best_split({blocks, keys, slots, rows, D, 3.0, key, 0.64}, cdiv(keys, 128));
+      // More blocks than run at once: those of the longest sequences first (100
+      // heads' sequences of 10 to 9000 tokens: 345 -> 273 us; 32 of 2000 to 8192 with
+      // weights 144 -> 132).  It costs 2 to 5 us: not where a window evens them out.
+      l.rows.by_length = even ? 0 : blocks * n > slots && !l.rows.pool_rows;
     }
   }
   l.nsplit = (int)std::max<int64_t>(n, 1);
@@ -131,15 +136,15 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   // one head's rows alone fill row tiles: heads need not share a tile
   const bool per_head = Nq >= 128;
   m.rows = CacheRows{per_head ? Nq : R, per_head ? B * H : B * Hk, per_head ? H / Hk : 1, 0,
-                     P > 0 && !pool, S > 0};
+                     P > 0 && !pool, S > 0, 0};
   // keys that a block of up to 256 rows can see at most
   int64_t own = (int64_t)sinks + window + (per_head ? 256 : Nq);
   if (own > S) own = S;
-  if (!pool || S > 0) cut(m, op, dtype, own + (m.rows.use_prefix ? P : 0), p->rows, D);
+  if (!pool || S > 0) cut(m, op, dtype, own + (m.rows.use_prefix ? P : 0), p->rows, D, own < S);
   p->slots = m.used ? m.nsplit / m.cluster : 0;
   if (pool) {
-    p->pooled.rows = CacheRows{B * R, Hk, 1, R, 1, 0};
-    cut(p->pooled, op, dtype, P, p->rows, D);
+    p->pooled.rows = CacheRows{B * R, Hk, 1, R, 1, 0, 0};
+    cut(p->pooled, op, dtype, P, p->rows, D, true);
     p->slots += p->pooled.nsplit / p->pooled.cluster;
   }
   // The weights need a row's whole sum: the kernel for few rows has it when one
@@ -151,11 +156,13 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   p->off_ml = 0;
   p->off_o = p->off_ml + ceil256(p->slots * p->rows * 8);
   p->off_lse = p->off_o + ceil256(p->slots * p->rows * D * 4);
-  p->off_logits = p->off_lse + (weights && (p->slots || !few) ? ceil256(p->rows * 4) : 0);
+  p->off_logits = p->off_lse + (weights && !few ? ceil256(p->rows * 4) : 0);
   if (p->rows > (int64_t(1) << 58) / (S + 1)) return AREA_EUNSUPPORTED;
   p->bytes = p->off_logits + (weights && few ? ceil256(p->rows * S * 4) : 0);
   const int64_t blocks = cdiv(m.rows.RG, 8) * m.rows.groups * std::max(m.nsplit, 1);
-  if (blocks > INT_MAX || cdiv(S, 128) * B * Hk > INT_MAX) return AREA_EUNSUPPORTED;
+  if (blocks > INT_MAX || cdiv(S, 128) * B * Hk > INT_MAX ||
+      (weights && few && p->rows + cdiv(S, 512) * B * Hk > INT_MAX))
+    return AREA_EUNSUPPORTED;
   return AREA_OK;
 }
 
@@ -186,7 +193,7 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     out.part_o = reinterpret_cast<float*>(w + p.off_o);
   }
   const bool weights = op == CACHE_OP_WEIGHTS, few = p.main.kernel == CACHE_DEC;
-  float* lse = weights && (p.slots || !few) ? reinterpret_cast<float*>(w + p.off_lse) : nullptr;
+  float* lse = weights && !few ? reinterpret_cast<float*>(w + p.off_lse) : nullptr;
   if (weights && few) {
     out.logits = reinterpret_cast<float*>(w + p.off_logits);
     out.acc = acc;
@@ -213,12 +220,11 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     out.slot0 += l->nsplit / l->cluster;
   }
   if (p.slots) {
-    e = launch_cache_join(a, out.part_o, out.part_ml, p.slots, p.rows, lse, dtype, s);
+    e = weights && few ? launch_cache_join_weights(a, out, p.slots, dtype, s)
+                       : launch_cache_join(a, out.part_o, out.part_ml, p.slots, p.rows, lse, dtype, s);
     if (e != cudaSuccess) return fail_cuda(e);
   }
-  if (!lse) return AREA_OK;
-  return finish(few ? launch_cache_weights(a, out.logits, lse, acc, acco, s)
-                    : launch_cache_weights_tc(a, lse, acc, acco, dtype, s));
+  return lse ? finish(launch_cache_weights_tc(a, lse, acc, acco, dtype, s)) : AREA_OK;
 }
 
 int ws_bytes_of(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int window, int sinks,

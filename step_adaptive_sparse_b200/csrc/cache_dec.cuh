@@ -36,6 +36,26 @@ struct DecSmem {
   __align__(16) float o[kDecWarps][ROWS][D];   // the block's in [0] in the end
 };
 
+// The group of a block whose place in the order is g: as it is, or the sequences
+// from the longest to the shortest, so that the last blocks to start are short
+// (up to as many sequences as the block has threads).
+__device__ __forceinline__ int dec_group(const CacheArgs& a, const CacheRows& rm, int g) {
+  if (!rm.by_length || !a.lens || a.B == 1 || a.B > kDecWarps * 32) return g;
+  __shared__ int s_len[kDecWarps * 32], s_b;
+  const int i = threadIdx.x, hk = g % a.Hk, want = g / a.Hk;
+  if (i < a.B) s_len[i] = cache_len(a, i);
+  __syncthreads();
+  if (i < a.B) {
+    const int n = s_len[i];
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < a.B; ++j) rank += s_len[j] > n || (s_len[j] == n && j < i);
+    if (rank == want) s_b = i;
+  }
+  __syncthreads();
+  return s_b * a.Hk + hk;
+}
+
 template <int D, int ROWS>
 __device__ __forceinline__ void dec_rows(DecSmem<D, ROWS>& sm, const CacheArgs& a,
                                          const CacheRows& rm, int g, int r0) {

@@ -7,33 +7,30 @@ namespace {
 
 // The row's output is
 //   sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s,   m = max_s m_s.
-// Many rows of few slots: a warp to a row; otherwise a block, whose warps take the
-// slots in turn and add up in shared memory in a fixed order (1024 rows of 8
-// slots: 6 us, with a warp to a row 11).  Four slots are loaded at once.  A slot without a key has l = 0
-// and its output, which nobody wrote, counts as zeros.
-constexpr int kJoinWarps = 8;
-template <typename T, int D, bool BLOCK>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-cache_join_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml, int slots,
-                  int64_t rows, T* o, float* lse) {
+// WARPS > 1: a block to a row, whose warps take the slots in turn and add up in
+// shared memory in a fixed order; otherwise a warp to a row.  Four slots are loaded
+// at once.  A slot without a key has l = 0 and its output, which nobody wrote,
+// counts as zeros.  A row without a weight has a log-sum of +inf, so that
+// 2^(x - lse) is 0 for every key.
+template <typename T, int D, int WARPS>
+__device__ __forceinline__ void join_row(const float* __restrict__ part_o,
+                                         const float2* __restrict__ part_ml, int slots,
+                                         int64_t rows, int64_t row, T* o, float* lse) {
   constexpr int kPer = D / 32;                             // columns of a lane
-  __shared__ float s_o[BLOCK ? kJoinWarps : 1][D], s_l[kJoinWarps];
+  __shared__ float s_o[WARPS][D], s_l[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kJoinWarps + warp;
-  if (row >= rows) return;                                 // !BLOCK: whole warps
   float m = -INFINITY;
   for (int s = lane; s < slots; s += 32) m = fmaxf(m, part_ml[s * rows + row].x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float ref = m == -INFINITY ? 0.f : m;
   float acc[kPer] = {}, l = 0.f;
-  constexpr int kStep = BLOCK ? kJoinWarps : 1;
-  for (int s0 = BLOCK ? warp : 0; s0 < slots; s0 += 4 * kStep) {
+  for (int s0 = WARPS > 1 ? warp : 0; s0 < slots; s0 += 4 * WARPS) {
     float x[4][kPer];
     float2 ml[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int s = s0 + i * kStep;
+      const int s = s0 + i * WARPS;
       ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) x[i][j] = 0.f;
@@ -57,14 +54,14 @@ cache_join_kernel(const float* __restrict__ part_o, const float2* __restrict__ p
       for (int j = 0; j < kPer; ++j) acc[j] = fmaf(w, any ? x[i][j] : 0.f, acc[j]);
     }
   }
-  if constexpr (BLOCK) {
+  if constexpr (WARPS > 1) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) s_o[warp][lane * kPer + j] = acc[j];
     if (lane == 0) s_l[warp] = l;
     __syncthreads();
     if (warp > 0) return;
     l = s_l[0];
-    for (int w = 1; w < kJoinWarps; ++w) {
+    for (int w = 1; w < WARPS; ++w) {
       l += s_l[w];
 #pragma unroll
       for (int j = 0; j < kPer; ++j) acc[j] += s_o[w][lane * kPer + j];
@@ -84,20 +81,44 @@ cache_join_kernel(const float* __restrict__ part_o, const float2* __restrict__ p
     for (int j = 0; j < kPer; j += 2)
       *reinterpret_cast<__nv_bfloat162*>(dst + j) = __floats2bfloat162_rn(acc[j], acc[j + 1]);
   }
-  // a row without a weight: +inf, so that 2^(x - lse) is 0 for every key
   if (lse && lane == 0) lse[row] = l == 0.f ? INFINITY : ref + log2f(l);
 }
 
-// kWKeys keys of a key head to a thread, a block apart; a key's rows' weights
-// are added in order.
-constexpr int kWThreads = 128, kWKeys = 4;
-__global__ void __launch_bounds__(kWThreads) cache_weights_kernel(const CacheArgs a,
-                                                                  const float* __restrict__ logits,
-                                                                  const float* __restrict__ lse,
-                                                                  const float* acc, float* acco,
-                                                                  int chunks) {
-  const int kvh = blockIdx.x / chunks;                       // (b, key head)
-  const int j0 = blockIdx.x % chunks * (kWThreads * kWKeys) + threadIdx.x;
+// Many rows of few slots: a warp to a row; otherwise a block (1024 rows of 8 slots:
+// 6 us, with a warp to a row 11).
+constexpr int kJoinWarps = 8;
+template <typename T, int D, bool BLOCK>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+cache_join_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml, int slots,
+                  int64_t rows, T* o, float* lse) {
+  const int64_t row = BLOCK ? (int64_t)blockIdx.x
+                            : (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (row >= rows) return;                                 // !BLOCK: whole warps
+  join_row<T, D, BLOCK ? kJoinWarps : 1>(part_o, part_ml, slots, rows, row, o, lse);
+}
+
+// The join for few rows of a key head, and the weights of its keys from the scores:
+// a grid's first blocks join a row each; the others have kWKeys keys of a key head
+// to a thread, a block apart, work out the rows' log-sums for themselves and add a
+// key's weights in the rows' order.  One launch instead of two, neither of which
+// fills the GPU (32 sequences of 8192 tokens, 8 key heads of 4 rows: 144 us in all,
+// with two launches 150).
+constexpr int kWThreads = 128, kWKeys = 4, kWRows = 24;
+template <typename T, int D>
+__global__ void __launch_bounds__(kWThreads)
+cache_join_weights_kernel(const CacheArgs a, const float* __restrict__ part_o,
+                          const float2* __restrict__ part_ml, int slots, int64_t rows,
+                          const float* __restrict__ logits, const float* acc, float* acco,
+                          int chunks) {
+  if (blockIdx.x < rows) {
+    join_row<T, D, kWThreads / 32>(part_o, part_ml, slots, rows, blockIdx.x, static_cast<T*>(a.o),
+                                   nullptr);
+    return;
+  }
+  __shared__ float s_lse[kWRows];
+  const int block = (int)(blockIdx.x - rows);
+  const int kvh = block / chunks;                            // (b, key head)
+  const int j0 = block % chunks * (kWThreads * kWKeys) + threadIdx.x;
   const int len = cache_len(a, kvh / a.Hk);
   const int R = a.H / a.Hk * a.Nq;
   const int64_t row0 = (int64_t)kvh * R, at = (int64_t)kvh * a.S;
@@ -107,11 +128,27 @@ __global__ void __launch_bounds__(kWThreads) cache_weights_kernel(const CacheArg
     const int j = j0 + x * kWThreads;
     old[x] = acc && j < a.S ? acc[at + j] : 0.f;
   }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp; r < R; r += kWThreads / 32) {
+    float m = -INFINITY, l = 0.f;
+    for (int s = lane; s < slots; s += 32) m = fmaxf(m, part_ml[s * rows + row0 + r].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int s = lane; s < slots; s += 32) {
+      const float2 ml = part_ml[s * rows + row0 + r];
+      if (ml.y != 0.f) l = fmaf(exp2f(ml.x - ref), ml.y, l);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    if (lane == 0) s_lse[r] = l == 0.f ? INFINITY : ref + log2f(l);
+  }
+  __syncthreads();
   int i = 0;
 #pragma unroll 4
   for (int r = 0; r < R; ++r) {
     const int end = len - a.Nq + 1 + i;                      // the row sees keys below it
-    const float z = lse[row0 + r];
+    const float z = s_lse[r];
     const float* src = logits + (row0 + r) * a.S + j0;
 #pragma unroll
     for (int x = 0; x < kWKeys; ++x)
@@ -146,11 +183,16 @@ cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const flo
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_weights(const CacheArgs& a, const float* logits, const float* lse,
-                                 const float* acc, float* acco, cudaStream_t s) {
+cudaError_t launch_cache_join_weights(const CacheArgs& a, const CacheOut& out, int slots, int dtype,
+                                      cudaStream_t s) {
+  if (a.H / a.Hk * a.Nq > kWRows) return cudaErrorInvalidValue;
   const int per = kWThreads * kWKeys, chunks = (a.S + per - 1) / per;
-  cache_weights_kernel<<<(unsigned)((int64_t)a.B * a.Hk * chunks), kWThreads, 0, s>>>(
-      a, logits, lse, acc, acco, chunks);
+  auto fn = dtype == AREA_DTYPE_F32
+                ? (a.D == 64 ? cache_join_weights_kernel<float, 64> : cache_join_weights_kernel<float, 128>)
+                : (a.D == 64 ? cache_join_weights_kernel<__nv_bfloat16, 64>
+                             : cache_join_weights_kernel<__nv_bfloat16, 128>);
+  fn<<<(unsigned)(out.rows + (int64_t)a.B * a.Hk * chunks), kWThreads, 0, s>>>(
+      a, out.part_o, out.part_ml, slots, out.rows, out.logits, out.acc, out.acco, chunks);
   return cudaGetLastError();
 }
 

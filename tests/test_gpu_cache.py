@@ -403,6 +403,69 @@ def test_eviction_without_lengths():
         assert all(torch.equal(x, y) for x, y in zip(out[0], o))
 
 
+@pytest.mark.parametrize("S,B,Hk", [(600, 40, 16), (300, 5, 60), (1500, 40, 16), (5000, 9, 16)])
+def test_eviction_of_many_heads(S, B, Hk):
+    """As many key heads as fill the GPU, so that fewer blocks share one."""
+    D, budget, sinks, recent = 64, S // 3, 4, S // 9
+    t, dt, _ = TYPES["bf16"]
+    g = torch.Generator().manual_seed(51)
+    k, v = (torch.randn(B, Hk, S, D, generator=g).to(t).cuda() for _ in range(2))
+    acc = weights_of("ties", (B, Hk, S), 52).cuda()
+    lens = [S - (i * 37) % S for i in range(B)]
+    dl = torch.tensor(lens, dtype=torch.int32).cuda()
+    ko, vo = (torch.zeros(B, Hk, budget, D, dtype=t, device="cuda") for _ in range(2))
+    acco = torch.full((B, Hk, budget), NAN, device="cuda")
+    lenso, idx = torch.zeros_like(dl), torch.zeros(B, Hk, budget, dtype=torch.int32, device="cuda")
+    area.area_cache_evict(k, v, acc, dl, ko, vo, acco, lenso, idx, B, Hk, S, budget, D, budget, sinks, recent, dt)
+    assert lenso.tolist() == [min(n, budget) for n in lens]
+    gi, host = idx.cpu(), acc.cpu()
+    for b, n in enumerate(lens):
+        for h in range(0, Hk, 7):
+            keep = co.kept_tokens(host[b, h].tolist(), n, budget, sinks, recent)
+            assert gi[b, h, :len(keep)].tolist() == keep and (gi[b, h, len(keep):] == -1).all()
+    had = idx >= 0
+    src = torch.where(had, idx, 0).long()
+    for x, y in ((k, ko), (v, vo)):
+        rows = x.gather(2, src[..., None].expand(-1, -1, -1, D))
+        assert torch.equal(torch.where(had[..., None], rows, 0), y)
+    assert torch.equal(torch.where(had, acc.gather(2, src), 0.0), acco)
+
+
+# ---- more sequences than run at once -----------------------------------------------------------
+
+def uneven(B, S):
+    """Lengths in no order, zeros, ones, equal ones and full ones among them."""
+    return [(i * i * 131 + 7 * i) % (S + 1) if i % 9 else (0, 1, S, S)[i // 9 % 4] for i in range(B)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S,D", [(70, 16, 8, 1, 300, 64), (128, 8, 4, 1, 131, 128), (129, 8, 4, 2, 70, 64),
+                                           (2, 240, 240, 1, 200, 64)])
+def test_many_sequences_of_uneven_lengths(B, H, Hk, Nq, S, D, dtype):
+    """The longest sequences' blocks start first: every call against the oracle."""
+    lens = uneven(B, S)
+    P = 33
+    dev, host, dl = make(61, dtype, B, H, Hk, Nq, S, D, lens, P=P)
+    scale = D ** -0.5
+    o = Guarded((B, H, Nq, D), TYPES[dtype][0], NAN)
+    run_sink(dev, dl, dtype, INT_MAX, 0, scale, o.t)
+    want, got, size = co.cache_attention(*host[:3], lens, scale)
+    close(o.t, want, bound(host, want, size, dtype, scale, S))
+    acc = torch.rand(B, Hk, S, generator=torch.Generator().manual_seed(62)).cuda()
+    acco = Guarded((B, Hk, S), torch.float32, NAN)
+    w = run_cache(dev, dl, dtype, scale, acc, o.t, acco.t)
+    close(o.t, want, bound(host, want, size, dtype, scale, S))
+    # as in test_cache_attention_and_weights
+    d = D * 2.0 ** -24 * scale * np.abs(host[0]).max() * np.nan_to_num(np.abs(host[1])).max() * D
+    sums = acc.double().cpu().numpy() + got
+    close(acco.t, sums, got * (4 * d + 2.0 ** -20) + (H // Hk * Nq + 2) * 2.0 ** -24 * sums)
+    run_prefix(dev, dl, dtype, 1, scale, o.t)
+    want, _, size = co.cache_attention(*host[:3], lens, scale, kp=host[3], vp=host[4])
+    close(o.t, want, bound(host, want, size, dtype, scale, P + S))
+    o.check(), acco.check(), w.check()
+    assert area.area_kernel_error() == 0
+
+
 # ---- together, on streams and in graphs -------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
