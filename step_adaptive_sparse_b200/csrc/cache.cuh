@@ -51,6 +51,7 @@ struct CacheOut {
   int nsplit;        // splits of this launch
   int cluster;       // splits that one cluster joins; the others' slots hold one split
   int slot0;         // its first slot in part_o / part_ml
+  int early;         // the launch may start before the call's last one is done
   int direct;        // 1: one split in all, the output is written to o
   float* part_o;     // [slots][rows][D]
   float2* part_ml;   // [slots][rows] (m, l)
@@ -151,7 +152,46 @@ __host__ __device__ __forceinline__ KeyList key_list(const CacheArgs& a, const C
   return l;
 }
 
+// A call's launches follow one another closely: a block of the next may start once
+// every block of this one has called let_next_start() or ended, and what it reads of
+// earlier launches it reads after wait_for_last(), which returns when those are
+// done.  Every launch that may start early waits before it ends, so that the end
+// of a call's last launch is the end of all.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_last() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---- host side ------------------------------------------------------------
+// Launches a kernel in clusters of `cluster` blocks; early: before the last launch of
+// the call is done (see let_next_start).
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cluster,
+                          bool early, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  cfg.attrs = at;
+  if (cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (early) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 enum { CACHE_OP_SINK, CACHE_OP_PREFIX, CACHE_OP_WEIGHTS };
 
 // The kernels: for few rows, for many rows.

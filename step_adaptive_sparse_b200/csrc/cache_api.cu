@@ -218,6 +218,7 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     }
     if (e != cudaSuccess) return fail_cuda(e);
     out.slot0 += l->nsplit / l->cluster;
+    out.early = 1;         // launches for other keys do not read one another's results
   }
   if (p.slots) {
     e = weights && few ? launch_cache_join_weights(a, out, p.slots, dtype, s)

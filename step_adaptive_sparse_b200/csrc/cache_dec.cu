@@ -65,6 +65,7 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
   const int n = lane >> 2, c = lane & 3;
   const int sp = blockIdx.x % out.nsplit;
   const int rb = blockIdx.x / out.nsplit % nrb;
+  let_next_start();
   const int g = dec_group(a, rm, blockIdx.x / out.nsplit / nrb);
   const int r0 = rb * kRows, r1 = min(r0 + kRows, rm.RG);
   const int kvh = rm.pool_rows ? 0 : g / rm.kv_div;           // (b, key head)

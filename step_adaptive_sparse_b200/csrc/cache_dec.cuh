@@ -158,24 +158,13 @@ __device__ __forceinline__ void dec_finish(DecSmem<D, ROWS>& sm, const CacheArgs
       out.acco[at + j] = out.acc ? out.acc[at + j] : 0.f;
   }
   if (cs > 1) cluster.sync();            // the others have read this block's sums
+  if (out.early) wait_for_last();
 }
 
-// Launches a kernel of these in clusters of out.cluster blocks.
 template <typename K>
 cudaError_t launch_dec(K kernel, int64_t grid, const CacheArgs& a, const CacheRows& rm,
                        const CacheOut& out, int nrb, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kDecWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)out.cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, rm, out, nrb);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_kernel(kernel, grid, kDecWarps * 32, 0, out.cluster, out.early, s, a, rm, out, nrb);
 }
 
 }  // namespace

@@ -70,6 +70,7 @@ cache_dec32_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, in
   const int grp = lane >> 3, c = lane & 7;   // keys 4 grp .. + 3 of a step
   const int sp = blockIdx.x % out.nsplit;
   const int rb = blockIdx.x / out.nsplit % nrb;
+  let_next_start();
   const int g = dec_group(a, rm, blockIdx.x / out.nsplit / nrb);
   const int r0 = rb * ROWS, r1 = min(r0 + ROWS, rm.RG);
   const int kvh = rm.pool_rows ? 0 : g / rm.kv_div;           // (b, key head)

@@ -11,10 +11,11 @@ namespace {
 // shared memory in a fixed order; otherwise a warp to a row.  Four slots are loaded
 // at once.  A slot without a key has l = 0 and its output, which nobody wrote,
 // counts as zeros.  A row without a weight has a log-sum of +inf, so that
-// 2^(x - lse) is 0 for every key.
+// 2^(x - lse) is 0 for every key.  (No __restrict__: nothing may be read before
+// wait_for_last.)
 template <typename T, int D, int WARPS>
-__device__ __forceinline__ void join_row(const float* __restrict__ part_o,
-                                         const float2* __restrict__ part_ml, int slots,
+__device__ __forceinline__ void join_row(const float* part_o,
+                                         const float2* part_ml, int slots,
                                          int64_t rows, int64_t row, T* o, float* lse) {
   constexpr int kPer = D / 32;                             // columns of a lane
   __shared__ float s_o[WARPS][D], s_l[WARPS];
@@ -89,8 +90,9 @@ __device__ __forceinline__ void join_row(const float* __restrict__ part_o,
 constexpr int kJoinWarps = 8;
 template <typename T, int D, bool BLOCK>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-cache_join_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml, int slots,
+cache_join_kernel(const float* part_o, const float2* part_ml, int slots,
                   int64_t rows, T* o, float* lse) {
+  wait_for_last();
   const int64_t row = BLOCK ? (int64_t)blockIdx.x
                             : (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
   if (row >= rows) return;                                 // !BLOCK: whole warps
@@ -106,10 +108,11 @@ cache_join_kernel(const float* __restrict__ part_o, const float2* __restrict__ p
 constexpr int kWThreads = 128, kWKeys = 4, kWRows = 24;
 template <typename T, int D>
 __global__ void __launch_bounds__(kWThreads)
-cache_join_weights_kernel(const CacheArgs a, const float* __restrict__ part_o,
-                          const float2* __restrict__ part_ml, int slots, int64_t rows,
-                          const float* __restrict__ logits, const float* acc, float* acco,
+cache_join_weights_kernel(const CacheArgs a, const float* part_o,
+                          const float2* part_ml, int slots, int64_t rows,
+                          const float* logits, const float* acc, float* acco,
                           int chunks) {
+  wait_for_last();
   if (blockIdx.x < rows) {
     join_row<T, D, kWThreads / 32>(part_o, part_ml, slots, rows, blockIdx.x, static_cast<T*>(a.o),
                                    nullptr);
@@ -163,24 +166,23 @@ cache_join_weights_kernel(const CacheArgs a, const float* __restrict__ part_o,
 }
 
 template <typename T>
-void join(const CacheArgs& a, const float* part_o, const float2* part_ml, int slots, int64_t rows,
+cudaError_t join(const CacheArgs& a, const float* part_o, const float2* part_ml, int slots, int64_t rows,
           float* lse, cudaStream_t s) {
   T* o = static_cast<T*>(a.o);
   const int threads = kJoinWarps * 32;
   const bool block = slots > 16 || rows <= 8192;
-  const unsigned grid = (unsigned)(block ? rows : (rows + kJoinWarps - 1) / kJoinWarps);
+  const int64_t grid = block ? rows : (rows + kJoinWarps - 1) / kJoinWarps;
   auto fn = a.D == 64 ? (block ? cache_join_kernel<T, 64, true> : cache_join_kernel<T, 64, false>)
                       : (block ? cache_join_kernel<T, 128, true> : cache_join_kernel<T, 128, false>);
-  fn<<<grid, threads, 0, s>>>(part_o, part_ml, slots, rows, o, lse);
+  return launch_kernel(fn, grid, threads, 0, 1, true, s, part_o, part_ml, slots, rows, o, lse);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const float2* part_ml,
                               int slots, int64_t rows, float* lse, int dtype, cudaStream_t s) {
-  if (dtype == AREA_DTYPE_F32) join<float>(a, part_o, part_ml, slots, rows, lse, s);
-  else join<__nv_bfloat16>(a, part_o, part_ml, slots, rows, lse, s);
-  return cudaGetLastError();
+  return dtype == AREA_DTYPE_F32 ? join<float>(a, part_o, part_ml, slots, rows, lse, s)
+                                 : join<__nv_bfloat16>(a, part_o, part_ml, slots, rows, lse, s);
 }
 
 cudaError_t launch_cache_join_weights(const CacheArgs& a, const CacheOut& out, int slots, int dtype,
@@ -191,9 +193,9 @@ cudaError_t launch_cache_join_weights(const CacheArgs& a, const CacheOut& out, i
                 ? (a.D == 64 ? cache_join_weights_kernel<float, 64> : cache_join_weights_kernel<float, 128>)
                 : (a.D == 64 ? cache_join_weights_kernel<__nv_bfloat16, 64>
                              : cache_join_weights_kernel<__nv_bfloat16, 128>);
-  fn<<<(unsigned)(out.rows + (int64_t)a.B * a.Hk * chunks), kWThreads, 0, s>>>(
-      a, out.part_o, out.part_ml, slots, out.rows, out.logits, out.acc, out.acco, chunks);
-  return cudaGetLastError();
+  return launch_kernel(fn, out.rows + (int64_t)a.B * a.Hk * chunks, kWThreads, 0, 1, true, s, a,
+                       out.part_o, out.part_ml, slots, out.rows, out.logits, out.acc, out.acco,
+                       chunks);
 }
 
 }  // namespace area

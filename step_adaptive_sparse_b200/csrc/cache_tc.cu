@@ -500,6 +500,8 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
       ++unit_count;
     }
   }
+  let_next_start();
+  if (prm.out.early) wait_for_last();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -522,8 +524,7 @@ cudaError_t launch(const Maps& maps, const UnitParams& prm, cudaStream_t s) {
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int grid = std::min(prm.units, num_sms());
-  fn<<<grid, kThreads, kSmem, s>>>(maps, prm);
-  return cudaGetLastError();
+  return launch_kernel(fn, grid, kThreads, kSmem, 1, prm.out.early, s, maps, prm);
 }
 
 }  // namespace

@@ -431,6 +431,8 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
       ++unit_count;
     }
   }
+  let_next_start();
+  if (prm.out.early) wait_for_last();
   tc_fence_before();
   __syncthreads();
   if (warp == kReadWarps) {
@@ -451,8 +453,7 @@ cudaError_t launch(const UnitParams& prm, cudaStream_t s) {
   if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  fn<<<std::min(prm.units, num_sms()), kThreads, kSmem, s>>>(prm);
-  return cudaGetLastError();
+  return launch_kernel(fn, std::min(prm.units, num_sms()), kThreads, kSmem, 1, prm.out.early, s, prm);
 }
 
 }  // namespace

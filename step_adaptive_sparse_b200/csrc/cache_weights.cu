@@ -133,6 +133,7 @@ cache_weights_tc_kernel(const __grid_constant__ WMaps tm, const __grid_constant_
     mbar_init(bar(W_DRAIN), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  wait_for_last();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(
                      smem_u32(&s_tmem_base))
@@ -281,6 +282,7 @@ cache_weights_tc32_kernel(const __grid_constant__ WParams p) {
     mbar_init(bar(W_DRAIN), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  wait_for_last();
   if (warp == 4) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(
                      smem_u32(&s_tmem_base))
@@ -411,8 +413,7 @@ cudaError_t launch_bf16(const WParams& p, int64_t grid, cudaStream_t s) {
   constexpr int kSmem = Geo<D>::kSmemBytes;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  fn<<<(unsigned)grid, kThreads, kSmem, s>>>(m, p);
-  return cudaGetLastError();
+  return launch_kernel(fn, grid, kThreads, kSmem, 1, true, s, m, p);
 }
 template <int D>
 cudaError_t launch_f32(const WParams& p, int64_t grid, cudaStream_t s) {
@@ -420,8 +421,7 @@ cudaError_t launch_f32(const WParams& p, int64_t grid, cudaStream_t s) {
   constexpr int kSmem = Geo32<D>::kSmemBytes;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  fn<<<(unsigned)grid, kThreads, kSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(fn, grid, kThreads, kSmem, 1, true, s, p);
 }
 
 }  // namespace

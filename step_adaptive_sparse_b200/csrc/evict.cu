@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs e, int 
   __shared__ int s_bin, s_above, s_gt, s_eq;   // kept keys above the threshold, equal to it, in lower ranks
   __shared__ int s_wgt[kWarps], s_weq[kWarps];
   __shared__ int s_list[kTile];
+  let_next_start();
   const auto cluster = cooperative_groups::this_cluster();
   const int64_t g = blockIdx.x / cs;
   const int rank = blockIdx.x % cs, b = (int)(g / e.Hk);
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs e, int 
 // of copy bandwidth).
 __global__ void __launch_bounds__(kThreads) evict_copy_kernel(const EvictArgs e,
                                                               int blocks_per_head) {
+  wait_for_last();
   const int64_t g = blockIdx.x / blocks_per_head;
   const int blk = blockIdx.x % blocks_per_head;
   const int m = min(evict_len(e, (int)(g / e.Hk)), e.budget);
@@ -241,6 +243,7 @@ __global__ void __launch_bounds__(kThreads) evict_copy_kernel(const EvictArgs e,
 // has one 64-byte column of K or V, or the weights, of a key head.
 constexpr int kMoveRows = 4;                             // rows of a thread and step
 __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs e, int cols) {
+  wait_for_last();
   const int g = blockIdx.x / (2 * cols + 1), part = blockIdx.x % (2 * cols + 1);
   const int n = evict_len(e, g / e.Hk), m = min(n, e.budget);
   const int* idx = e.idx + (int64_t)g * e.So;
@@ -304,27 +307,17 @@ cudaError_t launch_cache_evict(const EvictArgs& e, cudaStream_t s) {
   const int heads = e.B * e.Hk;
   const bool in_place = e.k == e.ko, one = !in_place && e.S <= kTile;
   const int cs = one ? evict_cluster(heads, e.S, 256, 4) : evict_cluster(heads, e.S, 1024, 8);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(heads * cs));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaError_t st = cudaLaunchKernelEx(&cfg, one ? evict_kernel<true> : evict_kernel<false>, e, cs);
-  if (st != cudaSuccess) return st;
+  cudaError_t st = launch_kernel(one ? evict_kernel<true> : evict_kernel<false>, (int64_t)heads * cs,
+                                 kThreads, 0, cs, false, s, e, cs);
+  if (st != cudaSuccess || one) return st;
   if (in_place) {
     const int cols = e.D * e.elem / 64;
-    evict_move_kernel<<<(unsigned)(heads * (2 * cols + 1)), 256, 0, s>>>(e, cols);
-  } else if (!one) {
-    const int per = kThreads / (e.D * e.elem / 16) * 2;  // rows of a block: two of each thread
-    const int nb = (e.budget + per - 1) / per;
-    evict_copy_kernel<<<(unsigned)((int64_t)heads * nb), kThreads, 0, s>>>(e, nb);
+    return launch_kernel(evict_move_kernel, (int64_t)heads * (2 * cols + 1), 256, 0, 1, true, s, e,
+                         cols);
   }
-  return cudaGetLastError();
+  const int per = kThreads / (e.D * e.elem / 16) * 2;    // rows of a block: two of each thread
+  const int nb = (e.budget + per - 1) / per;
+  return launch_kernel(evict_copy_kernel, (int64_t)heads * nb, kThreads, 0, 1, true, s, e, nb);
 }
 
 }  // namespace area
