@@ -10,6 +10,7 @@ library is missing the first call raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -121,6 +122,27 @@ def _lib() -> ctypes.CDLL:
             fn.argtypes = args
         _LIB = lib
     return _LIB
+
+
+_CALL_PATH = os.path.join(_HERE, "lib", "_areacall.so")
+_CALL = None
+
+
+def _call():
+    """The module that marshals the key/value cache's calls (see csrc/pycall.c)."""
+    global _CALL
+    if _CALL is None:
+        lib = _lib()
+        if not os.path.exists(_CALL_PATH):
+            raise ImportError(f"{_CALL_PATH} is missing; run "
+                              "`python -m step_adaptive_sparse_b200.build` first")
+        spec = importlib.util.spec_from_file_location("_areacall", _CALL_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        for name in mod.FUNCTIONS:
+            mod.bind(name, ctypes.cast(getattr(lib, name), _P).value)
+        _CALL = mod
+    return _CALL
 
 
 def library() -> ctypes.CDLL:
@@ -338,55 +360,53 @@ def area_window_attn_bridge(q, k, v, cand, R, cfg: area_plan_cfg, plan, plan_byt
                                           _stream(stream)), "area_window_attn_bridge")
 
 
+def _bytes(n: int, where: str) -> int:
+    if n < 0:
+        raise AreaError(-n, where)
+    return n
+
+
 def area_sink_attn_ws_bytes(B: int, H: int, Hk: int, Nq: int, S: int, D: int, window: int,
                             sinks: int, dtype: int) -> int:
-    out = _SZ(0)
-    _check(_lib().area_sink_attn_ws_bytes(B, H, Hk, Nq, S, D, window, sinks, dtype,
-                                          ctypes.byref(out)), "area_sink_attn_ws_bytes")
-    return out.value
+    return _bytes((_CALL or _call()).area_sink_attn_ws_bytes(B, H, Hk, Nq, S, D, window, sinks,
+                                                             dtype), "area_sink_attn_ws_bytes")
 
 
 def area_sink_attn(q, k, v, lens, o, ws, ws_bytes, B, H, Hk, Nq, S, D, window, sinks, scale, dtype,
                    stream=None) -> None:
-    _check(_lib().area_sink_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(o), _ptr(ws), ws_bytes,
-                                 B, H, Hk, Nq, S, D, window, sinks, scale, dtype,
-                                 _stream(stream)), "area_sink_attn")
+    _check((_CALL or _call()).area_sink_attn(q, k, v, lens, o, ws, ws_bytes, B, H, Hk, Nq, S, D,
+                                             window, sinks, scale, dtype, stream), "area_sink_attn")
 
 
 def area_prefix_attn_ws_bytes(B: int, H: int, Hk: int, Nq: int, P: int, S: int, D: int,
                               dtype: int) -> int:
-    out = _SZ(0)
-    _check(_lib().area_prefix_attn_ws_bytes(B, H, Hk, Nq, P, S, D, dtype, ctypes.byref(out)),
-           "area_prefix_attn_ws_bytes")
-    return out.value
+    return _bytes((_CALL or _call()).area_prefix_attn_ws_bytes(B, H, Hk, Nq, P, S, D, dtype),
+                  "area_prefix_attn_ws_bytes")
 
 
 def area_prefix_attn(q, kp, vp, k, v, lens, o, ws, ws_bytes, B, H, Hk, Nq, P, S, D, causal, scale,
                      dtype, stream=None) -> None:
-    _check(_lib().area_prefix_attn(_ptr(q), _ptr(kp), _ptr(vp), _ptr(k), _ptr(v), _ptr(lens),
-                                   _ptr(o), _ptr(ws), ws_bytes, B, H, Hk, Nq, P, S, D, causal,
-                                   scale, dtype, _stream(stream)), "area_prefix_attn")
+    _check((_CALL or _call()).area_prefix_attn(q, kp, vp, k, v, lens, o, ws, ws_bytes, B, H, Hk, Nq,
+                                               P, S, D, causal, scale, dtype, stream),
+           "area_prefix_attn")
 
 
 def area_cache_attn_ws_bytes(B: int, H: int, Hk: int, Nq: int, S: int, D: int, dtype: int) -> int:
-    out = _SZ(0)
-    _check(_lib().area_cache_attn_ws_bytes(B, H, Hk, Nq, S, D, dtype, ctypes.byref(out)),
-           "area_cache_attn_ws_bytes")
-    return out.value
+    return _bytes((_CALL or _call()).area_cache_attn_ws_bytes(B, H, Hk, Nq, S, D, dtype),
+                  "area_cache_attn_ws_bytes")
 
 
 def area_cache_attn(q, k, v, lens, acc, o, acco, ws, ws_bytes, B, H, Hk, Nq, S, D, scale, dtype,
                     stream=None) -> None:
-    _check(_lib().area_cache_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(acc), _ptr(o),
-                                  _ptr(acco), _ptr(ws), ws_bytes, B, H, Hk, Nq, S, D, scale,
-                                  dtype, _stream(stream)), "area_cache_attn")
+    _check((_CALL or _call()).area_cache_attn(q, k, v, lens, acc, o, acco, ws, ws_bytes, B, H, Hk,
+                                              Nq, S, D, scale, dtype, stream), "area_cache_attn")
 
 
 def area_cache_evict(k, v, acc, lens, ko, vo, acco, lenso, idx, B, Hk, S, So, D, budget, sinks,
                      recent, dtype, stream=None) -> None:
-    _check(_lib().area_cache_evict(_ptr(k), _ptr(v), _ptr(acc), _ptr(lens), _ptr(ko), _ptr(vo),
-                                   _ptr(acco), _ptr(lenso), _ptr(idx), B, Hk, S, So, D, budget,
-                                   sinks, recent, dtype, _stream(stream)), "area_cache_evict")
+    _check((_CALL or _call()).area_cache_evict(k, v, acc, lens, ko, vo, acco, lenso, idx, B, Hk, S,
+                                               So, D, budget, sinks, recent, dtype, stream),
+           "area_cache_evict")
 
 
 def parse_plan(buf: np.ndarray) -> dict:

@@ -8,12 +8,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libarea.so")
+CALL = os.path.join(LIBDIR, "_areacall.so")
 SOURCES = ["api.cu", "pool_dwt.cu", "plan.cu", "attn_simt.cu", "attn_tc.cu", "noalloc.cu",
            "bridge.cu", "schedule.cu", "cache_api.cu", "cache_dec.cu", "cache_dec32.cu",
            "cache_tc.cu", "cache_tc32.cu", "cache_weights.cu", "cache_join.cu", "evict.cu"]
@@ -70,7 +72,8 @@ def check_attn_resources(ptxas_log: str, kernel: str = "attn_tc_kernel") -> list
 
 
 def build(verbose: bool = False, jobs: int = 0) -> str:
-    """Compile every .cu of csrc/ into lib/libarea.so and return its path."""
+    """Compile every .cu of csrc/ into lib/libarea.so, and pycall.c into lib/_areacall.so; returns
+    the library's path."""
     os.makedirs(LIBDIR, exist_ok=True)
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -105,6 +108,9 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
         raise RuntimeError(f"nvcc failed:\n{msg}")
     link = [nvcc(), *ARCH, "-shared", "-o", LIB, *objs]
     subprocess.run(link, check=True)
+    # the CPython module that marshals the short calls
+    subprocess.run(["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+                    "-o", CALL, os.path.join(CSRC, "pycall.c")], check=True)
     return LIB
 
 

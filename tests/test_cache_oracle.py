@@ -209,3 +209,38 @@ def test_build_checks_the_tensor_core_kernel():
     assert len(b.check_attn_resources(log % (0, 160), "cache_tc_kernel")) == 1
     assert len(b.check_attn_resources(log % (8, 168), "cache_tc_kernel")) == 1
     assert len(b.check_attn_resources(log % (0, 168))) == 1
+
+
+def test_binding_of_the_cache_calls_refuses_what_it_cannot_pass(area, monkeypatch, tmp_path):
+    from step_adaptive_sparse_b200 import binding
+
+    class Address:                 # what a tensor and a stream offer
+        def __init__(self, at):
+            self.at, self.cuda_stream = at, 0
+
+        def data_ptr(self):
+            return self.at
+
+    good = [Address(32)] * 6 + [0, 1, 4, 2, 1, 64, 64, 8, 0, 0.125, 1]
+    with pytest.raises(area.AreaError) as e:           # a workspace too small or a bad scale get through to the call
+        area.area_sink_attn(*good[:15], -1.0, 1, Address(0))
+    assert e.value.status == area.AREA_EINVAL
+    with pytest.raises(TypeError):
+        area.area_sink_attn(*good[:7], "1", *good[8:])
+    with pytest.raises(TypeError):
+        area.area_sink_attn(*good[:7], 1.5, *good[8:])
+    with pytest.raises(AttributeError):
+        area.area_sink_attn("q", *good[1:])
+    with pytest.raises(AttributeError):
+        area.area_sink_attn(*good, "stream")
+    with pytest.raises(OverflowError):
+        area.area_sink_attn_ws_bytes(2 ** 31, 4, 2, 1, 64, 64, 8, 0, 1)
+    with pytest.raises(OverflowError):
+        area.area_sink_attn(*good[:6], -1, *good[7:])
+    import numpy as np
+    assert area.area_sink_attn_ws_bytes(np.int64(1), 8, 8, 1, 65536, 128, INT_MAX, 0, 1) == \
+        area.area_sink_attn_ws_bytes(1, 8, 8, 1, S=65536, D=128, window=INT_MAX, sinks=0, dtype=1)
+    monkeypatch.setattr(binding, "_CALL", None)
+    monkeypatch.setattr(binding, "_CALL_PATH", str(tmp_path / "_areacall.so"))
+    with pytest.raises(ImportError):
+        area.area_cache_attn_ws_bytes(1, 4, 2, 1, 64, 64, 1)
