@@ -105,9 +105,13 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D, b
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+struct Buf {               // null: none
+  const void* p;
+  int64_t n;
+};
+bool overlap(const Buf& a, const Buf& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
 }
 
 }  // namespace
@@ -183,6 +187,19 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     return AREA_EINVAL;
   if (ws_bytes < (size_t)p.bytes) return AREA_ENOSPACE;
   if ((p.bytes > 0 && !ws) || !aligned(ws, 32)) return AREA_EINVAL;
+  // what a call writes touches neither its inputs nor itself, except acco = acc
+  const int64_t e2 = dtype == AREA_DTYPE_F32 ? 4 : 2, most = int64_t(1) << 50;
+  const int64_t kv = std::min((int64_t)a.B * a.Hk * a.S, most), pre = std::min((int64_t)a.Hk * a.P, most);
+  const int64_t no = p.rows * a.D * e2, nkv = kv * a.D * e2, npre = pre * a.D * e2;
+  const Buf in[7] = {{a.q, no},     {a.k, nkv},   {a.v, nkv}, {a.kp, npre},
+                     {a.vp, npre}, {a.lens, a.B * 4ll}, {acc, kv * 4}};
+  const Buf to[3] = {{a.o, no}, {acco, kv * 4}, {ws, p.bytes}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 7; ++j)
+      if (!(i == 1 && j == 6 && acc == acco) && overlap(to[i], in[j])) return AREA_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(to[i], to[j])) return AREA_EINVAL;
+  }
   a.scale_log2 = scale * 1.4426950408889634f;
   char* w = static_cast<char*>(ws);
   CacheOut out{};
@@ -269,6 +286,7 @@ int area_prefix_attn(const void* q, const void* kp, const void* vp, const void* 
                      int Nq, int P, int S, int D, int causal, float scale, int dtype,
                      cudaStream_t stream) {
   if (causal != 0 && causal != 1) return AREA_EINVAL;
+  if (S == 0) lens = nullptr;              // not read: every sequence has no tokens of its own
   area::CacheArgs a{q, k, v, kp, vp, lens, o, B, H, Hk, Nq, P, S, D, INT_MAX, 0, causal, 0.f};
   return area::cache_call(area::CACHE_OP_PREFIX, a, scale, nullptr, nullptr, ws, ws_bytes, dtype,
                           stream);
@@ -315,16 +333,16 @@ int area_cache_evict(const void* k, const void* v, const float* acc, const int* 
   const bool in_place = k == ko || v == vo || acc == acco;
   if (in_place && (k != ko || v != vo || acc != acco || S != So)) return AREA_EINVAL;
   const int64_t nin = heads * S, nout = heads * So;
-  struct Buf { const void* p; int64_t n; };
+  using area::Buf;
   const Buf in[4] = {{k, nin * D * elem}, {v, nin * D * elem}, {acc, nin * 4}, {lens, lens ? B * 4ll : 0}};
   const Buf to[5] = {{lenso, B * 4ll}, {idx, nout * 4}, {ko, nout * D * elem},
                      {vo, nout * D * elem}, {acco, nout * 4}};
   for (int i = 0; i < 5; ++i) {
     for (int j = 0; j < 4; ++j)
-      if (!(in_place && i >= 2 && j == i - 2) && overlap(to[i].p, to[i].n, in[j].p, in[j].n))
+      if (!(in_place && i >= 2 && j == i - 2) && overlap(to[i], in[j]))
         return AREA_EINVAL;
     for (int j = 0; j < i; ++j)
-      if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return AREA_EINVAL;
+      if (overlap(to[i], to[j])) return AREA_EINVAL;
   }
   const area::EvictArgs e{k, v, acc, lens, ko, vo, acco, lenso, idx, B, Hk, S, So, D,
                           budget, sinks, recent, (int)elem};

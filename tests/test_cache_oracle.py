@@ -244,3 +244,34 @@ def test_binding_of_the_cache_calls_refuses_what_it_cannot_pass(area, monkeypatc
     monkeypatch.setattr(binding, "_CALL_PATH", str(tmp_path / "_areacall.so"))
     with pytest.raises(ImportError):
         area.area_cache_attn_ws_bytes(1, 4, 2, 1, 64, 64, 1)
+
+
+@pytest.mark.parametrize("op", ["sink", "prefix", "cache"])
+def test_overlapping_buffers_are_refused(area, op):
+    """Nothing is launched: the call that overlaps nowhere is refused for its
+    scale, as the last check but one."""
+    at = {n: A + i * FAR for i, n in enumerate(["q", "kp", "vp", "k", "v", "lens", "acc", "o", "acco", "ws"])}
+    sizes = {"q": 1 * 4 * 3 * 64 * 2, "k": 2 * 5000 * 64 * 2, "v": 2 * 5000 * 64 * 2, "kp": 2 * 40 * 64 * 2,
+             "vp": 2 * 40 * 64 * 2, "lens": 4, "acc": 2 * 5000 * 4}
+    names = {"sink": ["q", "k", "v", "lens", "o", "ws"], "prefix": ["q", "kp", "vp", "k", "v", "lens", "o", "ws"],
+             "cache": ["q", "k", "v", "lens", "acc", "o", "acco", "ws"]}[op]
+    size = {"sink": [1, 4, 2, 3, 5000, 64, 5000, 0], "prefix": [1, 4, 2, 3, 40, 5000, 64],
+            "cache": [1, 4, 2, 3, 5000, 64]}[op]
+    nb = getattr(area, f"area_{op}_attn_ws_bytes")(*size, 1)
+    assert nb > 0
+    call = getattr(area, f"area_{op}_attn")
+
+    def status(**moved):
+        args = [moved.get(n, at[n]) for n in names] + [nb, *size] + ([1] if op == "prefix" else [])
+        with pytest.raises(area.AreaError) as e:
+            call(*args, 1.0, 1, 0)
+        return e.value.status
+
+    for out in [n for n in ("o", "acco") if n in names]:
+        for inp in [n for n in names if n in sizes]:
+            assert status(**{out: at[inp]}) == EINVAL if (out, inp) != ("acco", "acc") else True
+            assert status(**{out: at[inp] + (sizes[inp] - 1) // 32 * 32}) == EINVAL, (out, inp)   # its last bytes
+        assert status(**{out: at["ws"] + 256}) == EINVAL
+    assert status(ws=at["k"] + 4096) == EINVAL
+    if op == "cache":
+        assert status(acco=at["o"] + 32) == EINVAL and status(acco=at["acc"] + 4) == EINVAL

@@ -565,6 +565,79 @@ def test_replayed_graphs_and_other_streams_give_the_same():
             assert all(torch.equal(x, y) for x, y in zip(o, e))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_replayed_graphs_of_prompts_and_of_an_eviction(dtype):
+    """Calls of several launches, captured one after the other without a wait
+    between them: replays follow the inputs, and two replays back to back leave
+    what an eager run leaves."""
+    B, H, Hk, S, D, Nq, P, budget = 2, 6, 2, 1500, 128, 70, 300, 600
+    dt = TYPES[dtype][1]
+    dev, _, dl = make(71, dtype, B, H, Hk, Nq, S, D, [1500, 1111], P=P, poison=False)
+    acc = torch.rand(B, Hk, S, device="cuda")
+    o = [torch.full_like(dev[0], NAN) for _ in range(3)]
+    acco = torch.full_like(acc, NAN)
+    ko, vo = (torch.zeros(B, Hk, budget, D, dtype=dev[1].dtype, device="cuda") for _ in range(2))
+    small, idx = torch.zeros(B, Hk, budget, device="cuda"), torch.zeros(B, Hk, budget, dtype=torch.int32, device="cuda")
+    lenso = torch.zeros_like(dl)
+    ws = [workspace(1 << 26) for _ in range(3)]
+    outs = [*o, acco, ko, vo, small, idx, lenso]
+
+    def step(s):
+        run_sink(dev, dl, dtype, INT_MAX, 0, 0.1, o[0], s, ws[0])
+        run_prefix(dev, dl, dtype, 1, 0.1, o[1], s, ws[1])
+        run_cache(dev, dl, dtype, 0.1, acc, o[2], acco, s, ws[2])
+        area.area_cache_evict(dev[1], dev[2], acco, dl, ko, vo, small, lenso, idx, B, Hk, S, budget, D, budget, 4, 99,
+                              dt, s)
+
+    stream = torch.cuda.Stream()
+    step(None)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        step(torch.cuda.current_stream())
+    for lens in ([1500, 1111], [70, 601], [3, 0]):
+        dl.copy_(torch.tensor(lens, dtype=torch.int32))
+        dev[0].mul_(-0.9)
+        step(None)
+        torch.cuda.synchronize()
+        want = [x.clone() for x in outs]
+        for x in outs[:4]:
+            x.fill_(NAN)
+        idx.fill_(5)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            g.replay()
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+    assert area.area_kernel_error() == 0
+
+
+def test_without_own_keys_lengths_are_not_read():
+    B, H, P, D = 3, 4, 2000, 64
+    dev, host, _ = make(72, "bf16", B, H, H, 1, 0, D, [0, 0, 0], P=P)
+    o = torch.full_like(dev[0], NAN)
+    run_prefix(dev, 16, "bf16", 0, 0.1, o)          # an address that holds nothing
+    want, _, size = co.cache_attention(*host[:3], [0] * B, 0.1, causal=False, kp=host[3], vp=host[4])
+    close(o, want, bound(host, want, size, "bf16", 0.1, P))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S,D", [(2, 4, 2, 5, 2, 64), (1, 4, 2, 33, 7, 128), (2, 2, 1, 300, 40, 64)])
+def test_more_queries_than_the_cache_has_room(B, H, Hk, Nq, S, D, dtype):
+    """Queries before the first token get rows of zeros, in every call."""
+    lens = [S, S // 2][:B]
+    dev, host, dl = make(73, dtype, B, H, Hk, Nq, S, D, lens, P=9)
+    for run, kw in ((lambda o: run_sink(dev, dl, dtype, 3, 1, 0.1, o), dict(window=3, sinks=1)),
+                    (lambda o: run_prefix(dev, dl, dtype, 1, 0.1, o), dict(kp=host[3], vp=host[4])),
+                    (lambda o: run_cache(dev, dl, dtype, 0.1, None, o, torch.zeros(B, Hk, S, device="cuda")), {})):
+        o = Guarded((B, H, Nq, D), TYPES[dtype][0], NAN)
+        run(o.t)
+        want, _, size = co.cache_attention(*host[:3], lens, 0.1, **kw)
+        close(o.t, want, bound(host, want, size, dtype, 0.1, S + 9))
+        o.check()
+
+
 def test_long_cache_offsets_past_32_bits():
     """A cache of more than 2^32 bytes and 2^31 values per tensor: the last
     sequence's rows lie past both."""
