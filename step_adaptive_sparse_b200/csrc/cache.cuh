@@ -196,6 +196,8 @@ enum { CACHE_OP_SINK, CACHE_OP_PREFIX, CACHE_OP_WEIGHTS };
 
 // The kernels: for few rows, for many rows.
 enum { CACHE_DEC, CACHE_TC };
+// Most rows of a key head whose scores the kernel for few rows leaves for the weights.
+constexpr int kCacheFewWeights = 24;
 // A launch of a call: the kernel, the rows and the splits of their keys.
 struct CacheLaunch {
   bool used;

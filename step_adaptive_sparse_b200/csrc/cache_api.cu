@@ -58,20 +58,51 @@ int64_t best_split(const SplitCost& c, int64_t most) {
   return best;
 }
 
-// Chooses a launch's kernel, and splits its keys (at most `keys` of them; even: most
-// sequences have as many).
-void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D, bool even) {
+// What the kernels for few and for many rows take, in us, for a launch of `groups`
+// groups of RG rows: a start, a further wave, and a block's or unit's keys; with
+// weights, the scores that few rows leave are read per row, those of many rows are
+// computed twice.  From runs of 2 to 256 groups of 12 to 64 rows and 50 to 8000 keys,
+// bf16 at D = 128 for example (few rows / many): 16 groups of 32 rows, 200 keys: 8.5 /
+// 10.8 us, 1000: 13.8 / 13.0, 8000: 38 / 22; 2 groups of 16, 1000 keys: 7.4 / 11.7;
+// 64 of 64, 200 keys: 20 / 15; with weights, 64 of 16, 500 keys: 24 / 21, 8000: 100 /
+// 119.
+struct KernelCost {
+  double few, few_row, few_key, many, many_key;
+};
+constexpr KernelCost kCost[2][2][2] = {                      // weights, fp32, D = 128
+    {{{5, 0, 3.1e-5, 8, 8.2e-5}, {5, 0, 6.0e-5, 8, 9.7e-5}},
+     {{7, 0, 9.4e-5, 12, 1.84e-4}, {8, 0, 1.7e-4, 15, 3.0e-4}}},
+    {{{8, 0.55, 5.8e-5, 13, 1.76e-4}, {8, 0.55, 8.6e-5, 13, 2.0e-4}},
+     {{10, 0.5, 1.1e-4, 14, 3.37e-4}, {10, 0.5, 1.95e-4, 18, 6.8e-4}}}};
+
+// Blocks of the kernel for few rows that run at once on an SM.
+int few_per_sm(int dtype, int D) {
+  return dtype == AREA_DTYPE_BF16 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
+}
+
+int choose_kernel(const CacheRows& rm, int op, int dtype, int64_t few_keys, int64_t many_keys, int D) {
+  const bool weights = op == CACHE_OP_WEIGHTS, f32 = dtype == AREA_DTYPE_F32;
+  // one block's rows: a row tile of 128 would be nearly empty
+  if (rm.RG <= 8) return CACHE_DEC;
+  if (weights && rm.RG > kCacheFewWeights) return CACHE_TC;
+  const KernelCost& c = kCost[weights][f32][D == 128];
+  const int64_t blocks = rm.groups * cdiv(rm.RG, rows_per_block(CACHE_DEC, dtype, rm));
+  const int64_t units = rm.groups * cdiv(rm.RG, rows_per_block(CACHE_TC, dtype, rm));
+  const double few = c.few + c.few_row * rm.RG + 5.0 * ((blocks - 1) / (few_per_sm(dtype, D) * kSms)) +
+                     c.few_key * (double)blocks * (double)few_keys;
+  const double many = c.many + 4.0 * ((units - 1) / kSms) + c.many_key * (double)units * (double)many_keys;
+  return few <= many ? CACHE_DEC : CACHE_TC;
+}
+
+// Chooses a launch's kernel, and splits its keys: at most few_keys or many_keys of
+// them, for a block of either kernel.  even: most sequences have as many.
+void cut(CacheLaunch& l, int op, int dtype, int64_t few_keys, int64_t many_keys, int64_t rows, int D,
+         bool even) {
   const int RG = l.rows.RG;
   l.used = true;
   l.cluster = 1;
-  // Few rows: the tensor-core kernels' 128-row tiles would be nearly empty.  Eight
-  // bf16 rows fill the products' narrow side; nine to 16 are as fast on either
-  // side for short caches and slower here for long ones (64 heads of 8000 keys:
-  // 81 us, there 62).  In fp32 16 rows take 11 us on 2000 keys, there 15, and
-  // 199 on the long ones, there 162; with weights, which there cost a second
-  // pass, 24 rows 148 us for 167, 32 rows 185 for 166.
-  l.kernel = RG <= (dtype == AREA_DTYPE_BF16 ? 8 : op == CACHE_OP_WEIGHTS ? 24 : 16) ? CACHE_DEC
-                                                                                     : CACHE_TC;
+  l.kernel = choose_kernel(l.rows, op, dtype, few_keys, many_keys, D);
+  const int64_t keys = l.kernel == CACHE_DEC ? few_keys : many_keys;
   const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, dtype, l.rows));
   int64_t n;
   if (l.kernel == CACHE_TC) {
@@ -80,8 +111,7 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D, b
     const double tile = dtype == AREA_DTYPE_BF16 ? 2.1 : D == 64 ? 3.2 : 5.6;
     n = best_split({blocks, keys, kSms, rows, D, 4.0, tile / 128, 1.0}, cdiv(keys, 256));
   } else {
-    const int per_sm = dtype == AREA_DTYPE_BF16 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
-    const int64_t slots = per_sm * kSms;
+    const int64_t slots = few_per_sm(dtype, D) * kSms;
     if (blocks * 8 <= slots && (keys <= 4096 || blocks * 8 >= 2 * kSms)) {
       // All blocks run at once: a cluster of up to 8 joins its splits itself
       // (4 heads of 500 keys: 6.0 us, with a join launch 7.1).  In larger grids
@@ -97,7 +127,7 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t keys, int64_t rows, int D, b
       // More blocks than run at once: those of the longest sequences first (100
       // heads' sequences of 10 to 9000 tokens: 345 -> 273 us; 32 of 2000 to 8192 with
       // weights 144 -> 132).  It costs 2 to 5 us: not where a window evens them out.
-      l.rows.by_length = even ? 0 : blocks * n > slots && !l.rows.pool_rows;
+      l.rows.by_length = even ? 0 : blocks * n > slots && !l.rows.pool_rows && l.rows.kv_div == 1;
     }
   }
   l.nsplit = (int)std::max<int64_t>(n, 1);
@@ -141,14 +171,16 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   const bool per_head = Nq >= 128;
   m.rows = CacheRows{per_head ? Nq : R, per_head ? B * H : B * Hk, per_head ? H / Hk : 1, 0,
                      P > 0 && !pool, S > 0, 0};
-  // keys that a block of up to 256 rows can see at most
-  int64_t own = (int64_t)sinks + window + (per_head ? 256 : Nq);
-  if (own > S) own = S;
-  if (!pool || S > 0) cut(m, op, dtype, own + (m.rows.use_prefix ? P : 0), p->rows, D, own < S);
+  // keys that a block of n rows can see at most
+  auto own = [&](int64_t n) {
+    return std::min<int64_t>(S, (int64_t)sinks + window + std::min<int64_t>(n, Nq));
+  };
+  const int64_t pk = m.rows.use_prefix ? P : 0;
+  if (!pool || S > 0) cut(m, op, dtype, own(per_head ? 8 : Nq) + pk, own(256) + pk, p->rows, D, own(256) < S);
   p->slots = m.used ? m.nsplit / m.cluster : 0;
   if (pool) {
     p->pooled.rows = CacheRows{B * R, Hk, 1, R, 1, 0, 0};
-    cut(p->pooled, op, dtype, P, p->rows, D, true);
+    cut(p->pooled, op, dtype, P, P, p->rows, D, true);
     p->slots += p->pooled.nsplit / p->pooled.cluster;
   }
   // The weights need a row's whole sum: the kernel for few rows has it when one

@@ -105,7 +105,7 @@ cache_join_kernel(const float* part_o, const float2* part_ml, int slots,
 // key's weights in the rows' order.  One launch instead of two, neither of which
 // fills the GPU (32 sequences of 8192 tokens, 8 key heads of 4 rows: 144 us in all,
 // with two launches 150).
-constexpr int kWThreads = 128, kWKeys = 4, kWRows = 24;
+constexpr int kWThreads = 128, kWKeys = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(kWThreads)
 cache_join_weights_kernel(const CacheArgs a, const float* part_o,
@@ -118,7 +118,7 @@ cache_join_weights_kernel(const CacheArgs a, const float* part_o,
                                    nullptr);
     return;
   }
-  __shared__ float s_lse[kWRows];
+  __shared__ float s_lse[kCacheFewWeights];
   const int block = (int)(blockIdx.x - rows);
   const int kvh = block / chunks;                            // (b, key head)
   const int j0 = block % chunks * (kWThreads * kWKeys) + threadIdx.x;
@@ -187,7 +187,7 @@ cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const flo
 
 cudaError_t launch_cache_join_weights(const CacheArgs& a, const CacheOut& out, int slots, int dtype,
                                       cudaStream_t s) {
-  if (a.H / a.Hk * a.Nq > kWRows) return cudaErrorInvalidValue;
+  if (a.H / a.Hk * a.Nq > kCacheFewWeights) return cudaErrorInvalidValue;
   const int per = kWThreads * kWKeys, chunks = (a.S + per - 1) / per;
   auto fn = dtype == AREA_DTYPE_F32
                 ? (a.D == 64 ? cache_join_weights_kernel<float, 64> : cache_join_weights_kernel<float, 128>)

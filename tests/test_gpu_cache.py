@@ -466,6 +466,56 @@ def test_many_sequences_of_uneven_lengths(B, H, Hk, Nq, S, D, dtype):
     assert area.area_kernel_error() == 0
 
 
+# ---- as many rows as the kernels for many rows are for ---------------------------------------
+
+MANY = [
+    # B, H, Hk, Nq, S, D, window, sinks, P, lens
+    (1, 64, 64, 130, 200, 64, 40, 5, 300, [200]),
+    (2, 40, 20, 257, 300, 128, 100, 7, 1, [300, 129]),
+    (1, 96, 32, 129, 129, 64, INT_MAX, 0, 65, [129]),
+    (3, 96, 32, 70, 150, 128, 33, 70, 140, [150, 69, 3]),
+    (1, 80, 80, 300, 420, 64, 256, 129, 128, [411]),
+    (2, 64, 64, 128, 128, 128, 1, 0, 31, [128, 0]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S,D,window,sinks,P,lens", MANY)
+def test_many_heads_of_many_rows(B, H, Hk, Nq, S, D, window, sinks, P, lens, dtype):
+    dev, host, dl = make(81, dtype, B, H, Hk, Nq, S, D, lens, P=P)
+    scale = D ** -0.5
+    o = Guarded((B, H, Nq, D), TYPES[dtype][0], NAN)
+    w = run_sink(dev, dl, dtype, window, sinks, scale, o.t)
+    want, _, size = co.cache_attention(*host[:3], lens, scale, window=window, sinks=sinks)
+    close(o.t, want, bound(host, want, size, dtype, scale, S))
+    w.check()
+    for causal in (0, 1):
+        w = run_prefix(dev, dl, dtype, causal, scale, o.t.fill_(NAN))
+        want, _, size = co.cache_attention(*host[:3], lens, scale, causal=bool(causal), kp=host[3], vp=host[4])
+        close(o.t, want, bound(host, want, size, dtype, scale, P + S))
+        w.check()
+    o.check()
+    assert area.area_kernel_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S,D", [(20, 12, 1, 1, 130, 64), (3, 48, 4, 2, 300, 128), (2, 16, 1, 1, 9001, 64),
+                                           (40, 24, 2, 1, 60, 128)])
+def test_weights_of_twelve_to_24_rows(B, H, Hk, Nq, S, D, dtype):
+    """Either kernel, as the sizes have it."""
+    lens = uneven(B, S)
+    dev, host, dl = make(82, dtype, B, H, Hk, Nq, S, D, lens)
+    o, acco = Guarded((B, H, Nq, D), TYPES[dtype][0], NAN), Guarded((B, Hk, S), torch.float32, NAN)
+    scale = D ** -0.5
+    w = run_cache(dev, dl, dtype, scale, None, o.t, acco.t)
+    want, got, size = co.cache_attention(*host[:3], lens, scale)
+    close(o.t, want, bound(host, want, size, dtype, scale, S))
+    # as in test_cache_attention_and_weights
+    d = D * 2.0 ** -24 * scale * np.abs(host[0]).max() * np.nan_to_num(np.abs(host[1])).max() * D
+    close(acco.t, got, got * (4 * d + 2.0 ** -20 + (H // Hk * Nq + 2) * 2.0 ** -24))
+    o.check(), acco.check(), w.check()
+
+
 # ---- together, on streams and in graphs -------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
