@@ -7,26 +7,27 @@ namespace {
 
 // The row's output is
 //   sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s,   m = max_s m_s.
-// WARPS > 1: a block to a row, whose warps take the slots in turn and add up in
-// shared memory in a fixed order; otherwise a warp to a row.  Four slots are loaded
-// at once.  A slot without a key has l = 0 and its output, which nobody wrote,
+// WARPS warps to a row take the slots in turn, four at once, and add up in shared
+// memory in a fixed order; a block of NW warps has NW / WARPS rows, from row0 on.  A slot without a key has l = 0 and its output, which nobody wrote,
 // counts as zeros.  A row without a weight has a log-sum of +inf, so that
 // 2^(x - lse) is 0 for every key.  (No __restrict__: nothing may be read before
 // wait_for_last.)
-template <typename T, int D, int WARPS>
-__device__ __forceinline__ void join_row(const float* part_o,
+template <typename T, int D, int WARPS, int NW>
+__device__ __forceinline__ void join_rows(const float* part_o,
                                          const float2* part_ml, int slots,
-                                         int64_t rows, int64_t row, T* o, float* lse) {
+                                         int64_t rows, int64_t row0, T* o, float* lse) {
   constexpr int kPer = D / 32;                             // columns of a lane
-  __shared__ float s_o[WARPS][D], s_l[WARPS];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float s_o[WARPS > 1 ? NW : 1][D], s_l[NW];
+  const int wid = threadIdx.x >> 5, warp = wid % WARPS, lane = threadIdx.x & 31;
+  const int64_t mine = row0 + wid / WARPS;
+  const int64_t row = mine < rows ? mine : rows - 1;       // behind the last: not written
   float m = -INFINITY;
   for (int s = lane; s < slots; s += 32) m = fmaxf(m, part_ml[s * rows + row].x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float ref = m == -INFINITY ? 0.f : m;
   float acc[kPer] = {}, l = 0.f;
-  for (int s0 = WARPS > 1 ? warp : 0; s0 < slots; s0 += 4 * WARPS) {
+  for (int s0 = warp; s0 < slots; s0 += 4 * WARPS) {
     float x[4][kPer];
     float2 ml[4];
 #pragma unroll
@@ -57,17 +58,18 @@ __device__ __forceinline__ void join_row(const float* part_o,
   }
   if constexpr (WARPS > 1) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) s_o[warp][lane * kPer + j] = acc[j];
-    if (lane == 0) s_l[warp] = l;
+    for (int j = 0; j < kPer; ++j) s_o[wid][lane * kPer + j] = acc[j];
+    if (lane == 0) s_l[wid] = l;
     __syncthreads();
     if (warp > 0) return;
-    l = s_l[0];
-    for (int w = 1; w < WARPS; ++w) {
-      l += s_l[w];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) acc[j] += s_o[w][lane * kPer + j];
+    for (int w = 1; w < WARPS; ++w) {
+      l += s_l[wid + w];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) acc[j] += s_o[wid + w][lane * kPer + j];
     }
   }
+  if (mine >= rows) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) acc[j] = l == 0.f ? 0.f : acc[j] * inv;
@@ -85,18 +87,14 @@ __device__ __forceinline__ void join_row(const float* part_o,
   if (lse && lane == 0) lse[row] = l == 0.f ? INFINITY : ref + log2f(l);
 }
 
-// Many rows of few slots: a warp to a row; otherwise a block (1024 rows of 8 slots:
-// 6 us, with a warp to a row 11).
 constexpr int kJoinWarps = 8;
-template <typename T, int D, bool BLOCK>
+template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 cache_join_kernel(const float* part_o, const float2* part_ml, int slots,
                   int64_t rows, T* o, float* lse) {
   wait_for_last();
-  const int64_t row = BLOCK ? (int64_t)blockIdx.x
-                            : (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= rows) return;                                 // !BLOCK: whole warps
-  join_row<T, D, BLOCK ? kJoinWarps : 1>(part_o, part_ml, slots, rows, row, o, lse);
+  join_rows<T, D, WARPS, kJoinWarps>(part_o, part_ml, slots, rows,
+                                     (int64_t)blockIdx.x * (kJoinWarps / WARPS), o, lse);
 }
 
 // The join for few rows of a key head, and the weights of its keys from the scores:
@@ -114,8 +112,8 @@ cache_join_weights_kernel(const CacheArgs a, const float* part_o,
                           int chunks) {
   wait_for_last();
   if (blockIdx.x < rows) {
-    join_row<T, D, kWThreads / 32>(part_o, part_ml, slots, rows, blockIdx.x, static_cast<T*>(a.o),
-                                   nullptr);
+    join_rows<T, D, kWThreads / 32, kWThreads / 32>(part_o, part_ml, slots, rows, blockIdx.x,
+                                                    static_cast<T*>(a.o), nullptr);
     return;
   }
   __shared__ float s_lse[kCacheFewWeights];
@@ -165,24 +163,30 @@ cache_join_weights_kernel(const CacheArgs a, const float* part_o,
   }
 }
 
-template <typename T>
-cudaError_t join(const CacheArgs& a, const float* part_o, const float2* part_ml, int slots, int64_t rows,
-          float* lse, cudaStream_t s) {
-  T* o = static_cast<T*>(a.o);
-  const int threads = kJoinWarps * 32;
-  const bool block = slots > 16 || rows <= 8192;
-  const int64_t grid = block ? rows : (rows + kJoinWarps - 1) / kJoinWarps;
-  auto fn = a.D == 64 ? (block ? cache_join_kernel<T, 64, true> : cache_join_kernel<T, 64, false>)
-                      : (block ? cache_join_kernel<T, 128, true> : cache_join_kernel<T, 128, false>);
-  return launch_kernel(fn, grid, threads, 0, 1, true, s, part_o, part_ml, slots, rows, o, lse);
+template <typename T, int D>
+cudaError_t join(const CacheArgs& a, const float* part_o, const float2* part_ml, int slots,
+                 int64_t rows, float* lse, cudaStream_t s) {
+  // four slots to a warp (calls with 6144 rows of 6: 41.6 us, with eight warps to a row 48;
+  // 128 rows of 7: 92.7, with one warp 100)
+  auto launch = [&](auto fn, int warps) {
+    const int64_t per = kJoinWarps / warps;
+    return launch_kernel(fn, (rows + per - 1) / per, kJoinWarps * 32, 0, 1, true, s, part_o, part_ml,
+                         slots, rows, static_cast<T*>(a.o), lse);
+  };
+  const int w = slots <= 4 ? 1 : slots <= 8 ? 2 : slots <= 16 ? 4 : 8;
+  if (w == 1) return launch(cache_join_kernel<T, D, 1>, 1);
+  if (w == 2) return launch(cache_join_kernel<T, D, 2>, 2);
+  if (w == 4) return launch(cache_join_kernel<T, D, 4>, 4);
+  return launch(cache_join_kernel<T, D, 8>, 8);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_join(const CacheArgs& a, const float* part_o, const float2* part_ml,
                               int slots, int64_t rows, float* lse, int dtype, cudaStream_t s) {
-  return dtype == AREA_DTYPE_F32 ? join<float>(a, part_o, part_ml, slots, rows, lse, s)
-                                 : join<__nv_bfloat16>(a, part_o, part_ml, slots, rows, lse, s);
+  auto fn = dtype == AREA_DTYPE_F32 ? (a.D == 64 ? join<float, 64> : join<float, 128>)
+                                    : (a.D == 64 ? join<__nv_bfloat16, 64> : join<__nv_bfloat16, 128>);
+  return fn(a, part_o, part_ml, slots, rows, lse, s);
 }
 
 cudaError_t launch_cache_join_weights(const CacheArgs& a, const CacheOut& out, int slots, int dtype,

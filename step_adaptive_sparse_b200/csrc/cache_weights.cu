@@ -6,9 +6,14 @@
 // and adds up 2^(s - lse) over the columns, in order: no sums across threads,
 // no atomics, and the scores never leave the SM (written out they would be
 // B H Nq S values: 16 heads' 256 queries on 60000 tokens are 1 GB).
+// Few keys: a cluster of blocks shares the rows of 128 keys, and its first block
+// adds their sums up in order (2 key heads of 1519 keys, 1024 rows, fp32: the call
+// 65 -> 43 us).
 // Tiles of rows that end before the block's keys are left out.  Keys that no
 // query sees may hold anything: a key's value stays in its own lane, which the
 // mask drops.
+#include <cooperative_groups.h>
+
 #include "cache.cuh"
 #include "cut3.cuh"
 #include "tc_common.cuh"
@@ -22,7 +27,8 @@ struct WParams {
   const float* acc;        // [B, Hk, S] or null
   float* acco;
   int R;                   // rows of a key head
-  int chunks;              // blocks of a key head
+  int chunks;              // clusters of a key head
+  int cs;                  // blocks of a cluster
 };
 
 // A tile of KR rows: those of [r0, r0 + n) see keys below hi0 at least and
@@ -83,6 +89,25 @@ __device__ __forceinline__ float add_tile(const WParams& p, RowTile rt, int j0, 
   }
   return sum;
 }
+// The cluster's sums, in the ranks' order, for the first block to write: own is this
+// block's for thread th's key.
+__device__ __forceinline__ void write_sums(const WParams& p, float own, float* s_part, int kvh, int j0,
+                                           int th, bool mine) {
+  const auto cluster = cooperative_groups::this_cluster();
+  const int rank = blockIdx.x % p.cs;
+  if (p.cs > 1) {
+    if (mine) s_part[th] = own;
+    cluster.sync();
+  }
+  const int j = j0 + th;
+  if (mine && rank == 0 && j < p.a.S) {
+    for (int r = 1; r < p.cs; ++r) own += *cluster.map_shared_rank(&s_part[th], r);
+    const int64_t at = (int64_t)kvh * p.a.S + j;
+    p.acco[at] = (p.acc ? p.acc[at] : 0.f) + own;
+  }
+  if (p.cs > 1) cluster.sync();          // the first block has read the others' sums
+}
+
 // ---- bf16: keys and rows by TMA -------------------------------------------
 constexpr int kThreads = 384;              // TMA, products, two groups of 128 keys' threads
 template <int D>
@@ -114,12 +139,15 @@ cache_weights_tc_kernel(const __grid_constant__ WMaps tm, const __grid_constant_
   __shared__ int s_abort;
   __shared__ __align__(16) float s_lse[2][128];
   __shared__ int s_hi[2][128];
-  __shared__ float s_sum[128];
+  __shared__ float s_sum[128], s_part[128];
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.x / p.chunks, j0 = blockIdx.x % p.chunks * 128;
+  const int block = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
+  const int kvh = block / p.chunks, j0 = block % p.chunks * 128;
   const int len = cache_len(p.a, kvh / p.a.Hk);
-  const int nrt = j0 < len ? (p.R + 127) / 128 : 0;
+  // this block's row tiles
+  const int all = j0 < len ? (p.R + 127) / 128 : 0;
+  const int rt0 = all * rank / p.cs, nrt = all * (rank + 1) / p.cs;
 
   if (threadIdx.x == 0) {
     s_abort = 0;
@@ -148,12 +176,12 @@ cache_weights_tc_kernel(const __grid_constant__ WMaps tm, const __grid_constant_
   float sum = 0.f;
 
   if (warp == 0) {
-    if (lane == 0 && nrt > 0) {
+    if (lane == 0 && nrt > rt0) {
       uint32_t it = 0;
       mbar_arrive_tx(bar(W_K_FULL), G::kTileBytes);
       for (int hf = 0; hf < G::kHalves; ++hf)
         tma_load_3d(sbase + hf * kHalfBytes, &tm.k, bar(W_K_FULL), hf * 64, j0, kvh);
-      for (int t = 0; t < nrt; ++t) {
+      for (int t = rt0; t < nrt; ++t) {
         if (row_tile<128>(p.a, p.R, len, t).hi1 <= j0) continue;
         const uint32_t b = it & 1u;
         if (!mbar_wait(bar(W_Q_EMPTY + b), ((it >> 1) & 1u) ^ 1u, abort_flag)) break;
@@ -173,8 +201,8 @@ cache_weights_tc_kernel(const __grid_constant__ WMaps tm, const __grid_constant_
     {
       uint32_t it = 0;
       const uint64_t dk = sdesc(sbase, 16, 1024), dq = sdesc(sbase + G::kSmemQ, 16, 1024);
-      bool ok = nrt == 0 || warp_wait_all(bar(W_K_FULL), 0, abort_flag);
-      for (int t = 0; t < nrt && ok; ++t) {
+      bool ok = nrt == rt0 || warp_wait_all(bar(W_K_FULL), 0, abort_flag);
+      for (int t = rt0; t < nrt && ok; ++t) {
         if (row_tile<128>(p.a, p.R, len, t).hi1 <= j0) continue;
         const uint32_t b = it & 1u, ph = (it >> 1) & 1u;
         if (!(ok = warp_wait_all(bar(W_Q_FULL + b), ph, abort_flag))) break;
@@ -205,7 +233,7 @@ cache_weights_tc_kernel(const __grid_constant__ WMaps tm, const __grid_constant_
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) << 5) << 16) + grp * 128;
     const int64_t row0 = (int64_t)kvh * p.R;
     uint32_t it = 0;
-    for (int t = 0; t < nrt; ++t) {
+    for (int t = rt0; t < nrt; ++t) {
       const RowTile rt = row_tile<128>(p.a, p.R, len, t);
       if (rt.hi1 <= j0) continue;
       const uint32_t ph = (it >> 1) & 1u;
@@ -224,12 +252,10 @@ cache_weights_tc_kernel(const __grid_constant__ WMaps tm, const __grid_constant_
   }
   tc_fence_before();
   __syncthreads();
-  if (warp >= 4 && warp < 8) {
-    const int j = j0 + threadIdx.x - 128;
-    if (j < p.a.S) {
-      const int64_t at = (int64_t)kvh * p.a.S + j;
-      p.acco[at] = (p.acc ? p.acc[at] : 0.f) + (sum + s_sum[threadIdx.x - 128]);
-    }
+  {
+    const bool mine = warp >= 4 && warp < 8;
+    const int th = mine ? threadIdx.x - 128 : 0;
+    write_sums(p, mine ? sum + s_sum[th] : 0.f, s_part, kvh, j0, th, mine);
   }
   if (warp == 1) {
     tc_fence_after();
@@ -264,11 +290,14 @@ cache_weights_tc32_kernel(const __grid_constant__ WParams p) {
   __shared__ int s_abort;
   __shared__ __align__(16) float s_lse[kKR32];
   __shared__ int s_hi[kKR32];
+  __shared__ float s_part[128];
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.x / p.chunks, j0 = blockIdx.x % p.chunks * 128;
+  const int block = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
+  const int kvh = block / p.chunks, j0 = block % p.chunks * 128;
   const int len = cache_len(p.a, kvh / p.a.Hk);
-  const int nrt = j0 < len ? (p.R + kKR32 - 1) / kKR32 : 0;
+  const int all = j0 < len ? (p.R + kKR32 - 1) / kKR32 : 0;
+  const int rt0 = all * rank / p.cs, nrt = all * (rank + 1) / p.cs;
 
   if (threadIdx.x == 0) {
     s_abort = 0;
@@ -294,9 +323,10 @@ cache_weights_tc32_kernel(const __grid_constant__ WParams p) {
   tc_fence_after();
   const uint32_t tmem = s_tmem_base;
   int* abort_flag = &s_abort;
+  float sum = 0.f;
 
   if (warp < 4) {
-    if (nrt > 0) {
+    if (nrt > rt0) {
       const int tid = threadIdx.x, ch = tid % kChunks, row0 = tid / kChunks;
       // 64 rows of a tensor from base on, n of them there, into registers and on
       // into an operand tile at `at`
@@ -326,7 +356,7 @@ cache_weights_tc32_kernel(const __grid_constant__ WParams p) {
       }
       mbar_arrive(bar(W_K_FULL));
       uint32_t it = 0;
-      for (int t = 0; t < nrt; ++t) {
+      for (int t = rt0; t < nrt; ++t) {
         const RowTile rt = row_tile<kKR32>(p.a, p.R, len, t);
         if (rt.hi1 <= j0) continue;
         const uint32_t b = it & 1u;
@@ -341,8 +371,8 @@ cache_weights_tc32_kernel(const __grid_constant__ WParams p) {
     {
       uint32_t it = 0;
       const uint64_t dk = sdesc(sbase, 16, 1024), dq = sdesc(sbase + G::kSmemQ, 16, 1024);
-      bool ok = nrt == 0 || warp_wait_all(bar(W_K_FULL), 0, abort_flag);
-      for (int t = 0; t < nrt && ok; ++t) {
+      bool ok = nrt == rt0 || warp_wait_all(bar(W_K_FULL), 0, abort_flag);
+      for (int t = rt0; t < nrt && ok; ++t) {
         if (row_tile<kKR32>(p.a, p.R, len, t).hi1 <= j0) continue;
         const uint32_t b = it & 1u, ph = (it >> 1) & 1u;
         if (!(ok = warp_wait_all(bar(W_Q_FULL + b), ph, abort_flag))) break;
@@ -373,9 +403,8 @@ cache_weights_tc32_kernel(const __grid_constant__ WParams p) {
     const int th = ((warp & 3) << 5) + lane;         // TMEM lane = key of the block
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) << 5) << 16);
     const int64_t row0 = (int64_t)kvh * p.R;
-    float sum = 0.f;
     uint32_t it = 0;
-    for (int t = 0; t < nrt; ++t) {
+    for (int t = rt0; t < nrt; ++t) {
       const RowTile rt = row_tile<kKR32>(p.a, p.R, len, t);
       if (rt.hi1 <= j0) continue;
       const uint32_t b = it & 1u, ph = (it >> 1) & 1u;
@@ -388,14 +417,13 @@ cache_weights_tc32_kernel(const __grid_constant__ WParams p) {
       mbar_arrive(bar(W_S_EMPTY + b));
       asm volatile("bar.sync 1, 128;" ::: "memory");
     }
-    const int j = j0 + th;
-    if (j < p.a.S) {
-      const int64_t at = (int64_t)kvh * p.a.S + j;
-      p.acco[at] = (p.acc ? p.acc[at] : 0.f) + sum;
-    }
   }
   tc_fence_before();
   __syncthreads();
+  {
+    const bool mine = warp >= 8;
+    write_sums(p, sum, s_part, kvh, j0, mine ? (int)threadIdx.x - 256 : 0, mine);
+  }
   if (warp == 4) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
@@ -413,7 +441,7 @@ cudaError_t launch_bf16(const WParams& p, int64_t grid, cudaStream_t s) {
   constexpr int kSmem = Geo<D>::kSmemBytes;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(fn, grid, kThreads, kSmem, 1, true, s, m, p);
+  return launch_kernel(fn, grid * p.cs, kThreads, kSmem, p.cs, true, s, m, p);
 }
 template <int D>
 cudaError_t launch_f32(const WParams& p, int64_t grid, cudaStream_t s) {
@@ -421,7 +449,7 @@ cudaError_t launch_f32(const WParams& p, int64_t grid, cudaStream_t s) {
   constexpr int kSmem = Geo32<D>::kSmemBytes;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(fn, grid, kThreads, kSmem, 1, true, s, p);
+  return launch_kernel(fn, grid * p.cs, kThreads, kSmem, p.cs, true, s, p);
 }
 
 }  // namespace
@@ -437,8 +465,12 @@ cudaError_t read_and_clear_cache_weights_error(int* code) {
 
 cudaError_t launch_cache_weights_tc(const CacheArgs& a, const float* lse, const float* acc,
                                     float* acco, int dtype, cudaStream_t s) {
-  const WParams p{a, lse, acc, acco, a.H / a.Hk * a.Nq, (a.S + 127) / 128};
+  WParams p{a, lse, acc, acco, a.H / a.Hk * a.Nq, (a.S + 127) / 128, 1};
   const int64_t grid = (int64_t)a.B * a.Hk * p.chunks;
+  // as many blocks as run at once, two row tiles to a block
+  const int tile = dtype == AREA_DTYPE_BF16 ? 128 : kKR32;
+  const int64_t most = dtype == AREA_DTYPE_BF16 ? 2 * num_sms() : num_sms();
+  while (p.cs < 8 && grid * p.cs * 2 <= most && p.R >= 4 * p.cs * tile) p.cs *= 2;
   if (dtype == AREA_DTYPE_BF16)
     return a.D == 64 ? launch_bf16<64>(p, grid, s) : launch_bf16<128>(p, grid, s);
   return a.D == 64 ? launch_f32<64>(p, grid, s) : launch_f32<128>(p, grid, s);
