@@ -51,6 +51,7 @@ struct CacheOut {
   int nsplit;        // splits of this launch
   int cluster;       // splits that one cluster joins; the others' slots hold one split
   int slot0;         // its first slot in part_o / part_ml
+  int warps;         // of a block of the kernels for few rows
   int early;         // the launch may start before the call's last one is done
   int direct;        // 1: one split in all, the output is written to o
   float* part_o;     // [slots][rows][D]
@@ -205,6 +206,7 @@ struct CacheLaunch {
   CacheRows rows;
   int nsplit;
   int cluster;
+  int warps;       // of a block of the kernels for few rows
 };
 // The launches of a call and the layout of its workspace; cache_plan computes
 // them from the sizes alone.

@@ -101,6 +101,7 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t few_keys, int64_t many_keys,
   const int RG = l.rows.RG;
   l.used = true;
   l.cluster = 1;
+  l.warps = 4;
   l.kernel = choose_kernel(l.rows, op, dtype, few_keys, many_keys, D);
   const int64_t keys = l.kernel == CACHE_DEC ? few_keys : many_keys;
   const int64_t blocks = l.rows.groups * cdiv(RG, rows_per_block(l.kernel, dtype, l.rows));
@@ -119,6 +120,12 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t few_keys, int64_t many_keys,
       // 8 splits: 214 us, without clusters 186).
       while (l.cluster < 8 && l.cluster * 128 < keys) l.cluster *= 2;
       n = l.cluster;
+      // Eight warps, fewer steps each, where every SM has one block at most (8 heads of
+      // 4000 keys, bf16: 12.9 -> 10.7 us, fp32 15.3 -> 13.5).  One block fills an SM's
+      // registers (bf16 with D = 64: half), so that more than 12 clusters of 8 may find no room
+      // in their part of the GPU (16 clusters: 14.6 -> 20.6 us).
+      const bool half = dtype == AREA_DTYPE_BF16 && D == 64;
+      if (blocks * n <= (half ? kSms : 96) && keys > 64 * n) l.warps = 8;
     } else {
       // all slots together read 6.3 TB/s (64 heads of 8000 keys in 6 splits, 0.86
       // waves: 51 us, in 8, 1.15 waves: 68)
@@ -256,6 +263,7 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     if (!l->used) continue;
     out.nsplit = l->nsplit;
     out.cluster = l->cluster;
+    out.warps = l->warps;
     switch (l->kernel) {
       case CACHE_TC:
         e = dtype == AREA_DTYPE_BF16 ? launch_cache_tc(a, l->rows, out, s)

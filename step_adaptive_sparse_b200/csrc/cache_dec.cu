@@ -1,8 +1,8 @@
 // Attention over a key/value cache for few query rows (bf16): one pass over
 // the keys, which is what bounds it.
 //
-// A block has up to 8 rows of a group and four warps, which take the keys
-// 16 at a time in turn.  The products are taken transposed, so that 8 rows
+// A block has up to 8 rows of a group and four warps (eight where the blocks do not
+// fill the GPU), which take the keys 16 at a time in turn.  The products are taken transposed, so that 8 rows
 // fill a whole mma.m16n8k16 and no row is padded beyond that:
 //   S^T (16 keys x 8 rows)    = K (16 x D)    Q^T (D x 8)
 //   O^T (D x 8 rows)          = V^T (D x 16)  P^T (16 x 8)
@@ -25,7 +25,6 @@ namespace {
 
 constexpr int kRows = 8;                     // rows of a block
 constexpr int kStep = 16;                    // keys of a warp and step
-constexpr int kTile = kDecWarps * kStep;        // keys of a block and step
 constexpr float kSlack = 8.f;                // log2 units
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -54,12 +53,13 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
   return v;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kDecWarps * 32, D == 64 ? 4 : 3)
+template <int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 1 : D == 64 ? 4 : 3)
 cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int nrb) {
+  constexpr int kTile = WARPS * kStep;       // keys of a block and step
   constexpr int kU = D / 32;                 // 16-byte loads of a thread per key row
   constexpr int kG = D / 64;                 // 16-byte loads of a thread per value row
-  __shared__ DecSmem<D, kRows> sm;
+  __shared__ DecSmem<D, kRows, WARPS> sm;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = lane >> 2, c = lane & 3;
@@ -244,7 +244,7 @@ template <int D>
 cudaError_t launch(const CacheArgs& a, const CacheRows& rm, const CacheOut& out, cudaStream_t s) {
   const int nrb = (rm.RG + kRows - 1) / kRows;
   const int64_t grid = (int64_t)rm.groups * nrb * out.nsplit;
-  return launch_dec(cache_dec_kernel<D>, grid, a, rm, out, nrb, s);
+  return launch_dec(out.warps == 8 ? cache_dec_kernel<D, 8> : cache_dec_kernel<D, 4>, grid, a, rm, out, nrb, s);
 }
 
 }  // namespace

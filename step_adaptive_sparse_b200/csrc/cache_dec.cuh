@@ -23,25 +23,25 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&f)[4]) {
                                             *reinterpret_cast<const uint32_t*>(&y));
 }
 
-constexpr int kDecWarps = 4;
+constexpr int kDecOrder = 128;            // sequences that a block can order
 
 // The rows of a block and its warps' results.
-template <int D, int ROWS>
+template <int D, int ROWS, int WARPS>
 struct DecSmem {
   int64_t row[ROWS];                     // -1: none
   KeySpan span[ROWS];
-  float m[kDecWarps][ROWS], l[kDecWarps][ROWS];
+  float m[WARPS][ROWS], l[WARPS][ROWS];
   float bm[ROWS], bl[ROWS];              // of the whole block
   float lse[ROWS];
-  __align__(16) float o[kDecWarps][ROWS][D];   // the block's in [0] in the end
+  __align__(16) float o[WARPS][ROWS][D];   // the block's in [0] in the end
 };
 
 // The group of a block whose place in the order is g: as it is, or the sequences
 // from the longest to the shortest, so that the last blocks to start are short
-// (up to as many sequences as the block has threads).
+// (up to kDecOrder sequences, as many as a block has threads).
 __device__ __forceinline__ int dec_group(const CacheArgs& a, const CacheRows& rm, int g) {
-  if (!rm.by_length || !a.lens || a.B == 1 || a.B > kDecWarps * 32) return g;
-  __shared__ int s_len[kDecWarps * 32], s_b;
+  if (!rm.by_length || !a.lens || a.B == 1 || a.B > kDecOrder) return g;
+  __shared__ int s_len[kDecOrder], s_b;
   const int i = threadIdx.x, hk = g % a.Hk, want = g / a.Hk;
   if (i < a.B) s_len[i] = cache_len(a, i);
   __syncthreads();
@@ -56,8 +56,8 @@ __device__ __forceinline__ int dec_group(const CacheArgs& a, const CacheRows& rm
   return s_b * a.Hk + hk;
 }
 
-template <int D, int ROWS>
-__device__ __forceinline__ void dec_rows(DecSmem<D, ROWS>& sm, const CacheArgs& a,
+template <int D, int ROWS, int WARPS>
+__device__ __forceinline__ void dec_rows(DecSmem<D, ROWS, WARPS>& sm, const CacheArgs& a,
                                          const CacheRows& rm, int g, int r0) {
   if (threadIdx.x < ROWS) {
     KeySpan s{0, 0};
@@ -80,10 +80,10 @@ __device__ __forceinline__ void dec_rows(DecSmem<D, ROWS>& sm, const CacheArgs& 
 // slot0 + sp / cluster size.  With out.acco the direct form then adds up the
 // weights of the block's own keys [j0, j1), whose scores it has left in
 // out.logits, and copies its share of the sums behind the last token.
-template <typename T, int D, int ROWS>
-__device__ __forceinline__ void dec_finish(DecSmem<D, ROWS>& sm, const CacheArgs& a,
+template <typename T, int D, int ROWS, int WARPS>
+__device__ __forceinline__ void dec_finish(DecSmem<D, ROWS, WARPS>& sm, const CacheArgs& a,
                                            const CacheOut& out, int sp, int kvh, int j0, int j1) {
-  constexpr int kThreads = kDecWarps * 32, kVecs = ROWS * (D / 4);
+  constexpr int kThreads = WARPS * 32, kVecs = ROWS * (D / 4);
   const auto cluster = cooperative_groups::this_cluster();
   const int cs = out.cluster, rank = sp % cs, tid = threadIdx.x;
   __syncthreads();
@@ -91,11 +91,11 @@ __device__ __forceinline__ void dec_finish(DecSmem<D, ROWS>& sm, const CacheArgs
     const int r = e / (D / 4), d = e % (D / 4) * 4;
     float mm = sm.m[0][r];
 #pragma unroll
-    for (int w = 1; w < kDecWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
+    for (int w = 1; w < WARPS; ++w) mm = fmaxf(mm, sm.m[w][r]);
     const float ref = mm == -INFINITY ? 0.f : mm;
     float ll = 0.f, f[4] = {};
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const float al = ex2(sm.m[w][r] - ref);
       ll = fmaf(al, sm.l[w][r], ll);
       const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][d]);
@@ -164,7 +164,7 @@ __device__ __forceinline__ void dec_finish(DecSmem<D, ROWS>& sm, const CacheArgs
 template <typename K>
 cudaError_t launch_dec(K kernel, int64_t grid, const CacheArgs& a, const CacheRows& rm,
                        const CacheOut& out, int nrb, cudaStream_t s) {
-  return launch_kernel(kernel, grid, kDecWarps * 32, 0, out.cluster, out.early, s, a, rm, out, nrb);
+  return launch_kernel(kernel, grid, out.warps * 32, 0, out.cluster, out.early, s, a, rm, out, nrb);
 }
 
 }  // namespace

@@ -1,8 +1,8 @@
 // Attention over a key/value cache for few query rows (fp32): one pass over
 // the keys on the CUDA cores.
 //
-// A block has ROWS rows of a group and four warps, which take the keys 16 at a
-// time in turn, straight from global memory into registers:
+// A block has ROWS rows of a group and four warps (eight where the blocks do not
+// fill the GPU), which take the keys 16 at a time in turn, straight from global memory into registers:
 //   scores  eight lanes to a key and four keys to a lane: a lane multiplies
 //           its 16-byte pieces of the keys with those of the rows (shared
 //           memory, one broadcast read per piece and four keys), and the
@@ -21,7 +21,6 @@ namespace area {
 namespace {
 
 constexpr int kStep = 16;                    // keys of a warp and step
-constexpr int kTile = kDecWarps * kStep;     // keys of a block and step
 constexpr float kSlack = 8.f;                // log2 units
 
 // Keys and values are read once: they need no place in L1.
@@ -57,14 +56,15 @@ __device__ __forceinline__ void reduce_halves(float* v, int lane) {
   if constexpr (BIT > 1) reduce_halves<N / 2, BIT / 2>(v, lane);
 }
 
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kDecWarps * 32, 2)
+template <int D, int ROWS, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 1 : 2)
 cache_dec32_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int nrb) {
+  constexpr int kTile = WARPS * kStep;       // keys of a block and step
   constexpr int kU = D / 32;                 // 16-byte pieces of a lane per key
   constexpr int kW = D / 32;                 // value columns of a lane
   constexpr int kOwn = ROWS / 2;             // scores of a lane after the exchange
-  __shared__ DecSmem<D, ROWS> sm;
-  __shared__ __align__(16) float s_q[ROWS][D], s_p[kDecWarps][kStep][ROWS];
+  __shared__ DecSmem<D, ROWS, WARPS> sm;
+  __shared__ __align__(16) float s_q[ROWS][D], s_p[WARPS][kStep][ROWS];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane >> 3, c = lane & 7;   // keys 4 grp .. + 3 of a step
@@ -115,7 +115,7 @@ cache_dec32_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, in
     load_v(u0);
   }
   dec_rows(sm, a, rm, g, r0);
-  for (int e = threadIdx.x; e < ROWS * (D / 4); e += kDecWarps * 32) {
+  for (int e = threadIdx.x; e < ROWS * (D / 4); e += WARPS * 32) {
     const int r = e / (D / 4), d = e % (D / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (sm.row[r] >= 0)
@@ -232,8 +232,8 @@ cache_dec32_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, in
 template <int D, int ROWS>
 cudaError_t launch(const CacheArgs& a, const CacheRows& rm, const CacheOut& out, cudaStream_t s) {
   const int nrb = (rm.RG + ROWS - 1) / ROWS;
-  return launch_dec(cache_dec32_kernel<D, ROWS>, (int64_t)rm.groups * nrb * out.nsplit, a, rm, out,
-                    nrb, s);
+  return launch_dec(out.warps == 8 ? cache_dec32_kernel<D, ROWS, 8> : cache_dec32_kernel<D, ROWS, 4>,
+                    (int64_t)rm.groups * nrb * out.nsplit, a, rm, out, nrb, s);
 }
 
 template <int D>
