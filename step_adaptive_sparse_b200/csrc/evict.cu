@@ -170,7 +170,51 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs e, int 
   asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   // keys above the threshold are kept, and the first `left` of those equal to it
   int gt0 = s_gt, eq0 = s_eq;    // found so far
-  for (int j0 = c0; j0 < c1; j0 += kTile) {
+  if constexpr (kHeld > 0) {
+    // those in registers: every warp's counts of every step, their sums before it
+    __shared__ int s_cnt[kHeld * kWarps], s_sum;         // above in the low half, equal in the high
+    const unsigned below = (1u << lane) - 1;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const bool in = c0 + tid + i * kThreads < c1;
+      const unsigned gt = __ballot_sync(0xffffffffu, in && held[i] > prefix);
+      const unsigned eq = __ballot_sync(0xffffffffu, in && held[i] == prefix);
+      if (lane == 0) s_cnt[i * kWarps + warp] = __popc(gt) | __popc(eq) << 16;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      constexpr int kOwn = kHeld * kWarps / 32;
+      int c[kOwn], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) c[i] = s_cnt[lane * kOwn + i], sum += c[i];
+      int incl = sum;
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, x);
+        if (lane >= x) incl += t;
+      }
+      int before = incl - sum;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        s_cnt[lane * kOwn + i] = before;
+        before += c[i];
+      }
+      if (lane == 31) s_sum = incl;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int j = c0 + tid + i * kThreads;
+      const bool is_gt = j < c1 && held[i] > prefix, is_eq = j < c1 && held[i] == prefix;
+      const unsigned gt = __ballot_sync(0xffffffffu, is_gt), eq = __ballot_sync(0xffffffffu, is_eq);
+      const int base = s_cnt[i * kWarps + warp];
+      const int gtb = gt0 + (base & 0xffff) + __popc(gt & below);
+      const int eqb = eq0 + (base >> 16) + __popc(eq & below);
+      if (is_gt || (is_eq && eqb < left)) idx[e.sinks + gtb + min(eqb, left)] = e.sinks + j;
+    }
+    gt0 += s_sum & 0xffff, eq0 += s_sum >> 16;
+  }
+  for (int j0 = c0 + kHeld * kThreads; j0 < c1; j0 += kTile) {
     const int j = j0 + tid * kPer;
     float w[kPer];
     uint32_t gt = 0, eq = 0;     // one bit per candidate of the thread
