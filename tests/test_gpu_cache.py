@@ -476,6 +476,9 @@ MANY = [
     (3, 96, 32, 70, 150, 128, 33, 70, 140, [150, 69, 3]),
     (1, 80, 80, 300, 420, 64, 256, 129, 128, [411]),
     (2, 64, 64, 128, 128, 128, 1, 0, 31, [128, 0]),
+    # few queries on a long cache: the rows of a key head's heads share row tiles
+    (2, 8, 2, 130, 3000, 64, INT_MAX, 0, 500, [3000, 135]),
+    (1, 6, 1, 300, 2500, 128, 2499, 1, 64, [2100]),
 ]
 
 
