@@ -144,6 +144,10 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
              (span[x].hi - kl.lo == kl.total - kl.np - kl.ns && span[x].lo == kl.lo));
   }
   all = __all_sync(0xffffffffu, all);
+  float* score[2];               // where key 0's scores of these rows go
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    score[x] = out.logits && sm.row[2 * c + x] >= 0 ? out.logits + sm.row[2 * c + x] * a.S : nullptr;
 
   float o[kG * 4][4], m[2], l[2];
 #pragma unroll
@@ -167,14 +171,14 @@ cache_dec_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, int 
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       s[x] *= a.scale_log2;
-      if (!whole || out.logits) {
+      if (whole) {
+        // (with scores the list is the cache's first keys)
+        if (score[x & 1]) score[x & 1][u0 + n + 8 * (x >> 1)] = s[x];
+      } else {
         const int u = u0 + n + 8 * (x >> 1), w = u - kl.np;
         const int key = w < kl.ns ? w : kl.lo + (w - kl.ns);
         const bool in = u < uend && (u < kl.np ? pre[x & 1] : sees_own(a, span[x & 1], key));
-        if (out.logits && in) {
-          const int64_t row = sm.row[2 * c + (x & 1)];
-          if (row >= 0) out.logits[row * a.S + key] = s[x];
-        }
+        if (score[x & 1] && in) score[x & 1][key] = s[x];
         if (!in) s[x] = -INFINITY;
       }
       grow = grow || s[x] > m[x & 1] + kSlack;

@@ -130,6 +130,7 @@ cache_dec32_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, in
   const int row = c * kOwn / 4, key0 = c * kOwn % 4;
   const KeySpan span = sm.span[row];
   const bool valid = sm.row[row] >= 0, pre = valid && sees_prefix(a, span);
+  float* const score = out.logits && valid ? out.logits + sm.row[row] * a.S : nullptr;
   float o[ROWS][kW], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int r = 0; r < ROWS; ++r)
@@ -162,7 +163,7 @@ cache_dec32_kernel(const CacheArgs a, const CacheRows rm, const CacheOut out, in
       const int u = u0 + grp * 4 + key0 + i, w = u - kl.np;
       const int key = w < kl.ns ? w : kl.lo + (w - kl.ns);
       const bool in = valid && u < uend && (u < kl.np ? pre : sees_own(a, span, key));
-      if (out.logits && in) out.logits[sm.row[row] * a.S + key] = s[i];
+      if (score && in) score[key] = s[i];
       if (!in) s[i] = -INFINITY;
       top = fmaxf(top, s[i]);
     }
