@@ -484,8 +484,7 @@ int area_window_attn_noalloc(const void* q, const void* k, const void* v,
  *     and in CUDA-graph replays.
  *   - scale is positive.  dtype: bf16 or fp32; D: 64 or 128.
  * Errors of all of them: AREA_EINVAL (null, bad size, misaligned or
- * overlapping buffer),
- * AREA_EUNSUPPORTED (dtype, D, or sizes past 32-bit row
+ * overlapping buffer), AREA_EUNSUPPORTED (dtype, D, or sizes past 32-bit row
  * indexes: B * H * Nq, P + S above 2^31 - 257), AREA_ENOSPACE, AREA_ECUDA.
  */
 
@@ -515,8 +514,8 @@ int area_sink_attn(const void* q, const void* k, const void* v,
  *               images of one prompt that share its text keys)
  * P = 0 (kp, vp null) or S = 0 (k, v null; lens is then not read) leave that
  * part out; one of them is positive.  When a sequence has few queries (fewer
- * than 64 rows per key head) the prefix is read once for the batch, all
- * sequences' rows against it, and joined with the own keys' part.
+ * than 64 rows per key head) and the prefix is long, it is read once for the
+ * batch, all sequences' rows against it, and joined with the own keys' part.
  */
 int area_prefix_attn_ws_bytes(int B, int H, int Hk, int Nq, int P, int S,
                               int D, int dtype, size_t* ws_bytes);

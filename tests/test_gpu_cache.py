@@ -666,6 +666,29 @@ def test_replayed_graphs_of_prompts_and_of_an_eviction(dtype):
     assert area.area_kernel_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S,D", [(3, 8, 2, 5, 90, 64), (2, 8, 2, 40, 700, 128), (2, 48, 48, 200, 300, 64)])
+def test_queries_before_the_first_token_may_hold_anything(B, H, Hk, Nq, S, D, dtype):
+    """Padding in front is NaN: rows of zeros, and nothing of it in the others or in the weights."""
+    lens = [S, Nq // 2, 1][:B]
+    dev, host, dl = make(91, dtype, B, H, Hk, Nq, S, D, lens, P=50)
+    for b, n in enumerate(lens):
+        dev[0][b, :, :max(0, Nq - n)] = NAN
+    o, acco = Guarded((B, H, Nq, D), TYPES[dtype][0], NAN), Guarded((B, Hk, S), torch.float32, NAN)
+    for run, kw in ((lambda: run_sink(dev, dl, dtype, 30, 2, 0.1, o.t), dict(window=30, sinks=2)),
+                    (lambda: run_prefix(dev, dl, dtype, 1, 0.1, o.t), dict(kp=host[3], vp=host[4])),
+                    (lambda: run_cache(dev, dl, dtype, 0.1, None, o.t, acco.t), {})):
+        run()
+        want, got, size = co.cache_attention(*host[:3], lens, 0.1, **kw)
+        close(o.t, want, bound(host, want, size, dtype, 0.1, S + 50))
+        for b, n in enumerate(lens):
+            assert (o.t[b, :, :max(0, Nq - n)] == 0).all()
+    # as in test_cache_attention_and_weights
+    d = D * 2.0 ** -24 * 0.1 * np.abs(host[0]).max() * np.nan_to_num(np.abs(host[1])).max() * D
+    close(acco.t, got, got * (4 * d + 2.0 ** -20 + (H // Hk * Nq + 2) * 2.0 ** -24))
+    o.check(), acco.check()
+
+
 def test_without_own_keys_lengths_are_not_read():
     B, H, P, D = 3, 4, 2000, 64
     dev, host, _ = make(72, "bf16", B, H, H, 1, 0, D, [0, 0, 0], P=P)
