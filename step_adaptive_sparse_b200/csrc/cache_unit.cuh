@@ -32,6 +32,7 @@ struct UnitParams {
   int tiles;               // row tiles of a unit
   int units;
   int heavy_first;         // row tiles from the last to the first, over all groups
+  int halved;              // the last units come as two, of one row tile each
 };
 
 // A key tile of a unit.
@@ -102,6 +103,8 @@ __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& 
   const CacheArgs& a = p.a;
   const CacheRows& rm = p.rm;
   if (idx >= p.units) return false;
+  const int in_halves = idx - (p.units - 2 * p.halved), half = in_halves & 1;
+  if (in_halves >= 0) idx -= in_halves - in_halves / 2;
   u.sp = idx % p.out.nsplit;
   const int rest = idx / p.out.nsplit;
   int rb;
@@ -113,12 +116,17 @@ __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& 
     u.g = rest / p.nrb;
   }
   u.r0[0] = rb * p.tiles * p.tile_rows;
-  u.r0[1] = min(u.r0[0] + p.tile_rows, rm.RG);
-  const int r1 = min(u.r0[0] + p.tiles * p.tile_rows, rm.RG);
+  int r1 = min(u.r0[0] + p.tiles * p.tile_rows, rm.RG);
+  const int k0 = u.r0[0], k1 = r1;               // a half has its unit's list, cut as its unit's
+  if (in_halves >= 0) {
+    u.r0[0] = min(u.r0[0] + half * p.tile_rows, rm.RG);
+    r1 = min(u.r0[0] + p.tile_rows, rm.RG);
+  }
+  u.r0[1] = in_halves >= 0 ? rm.RG : min(u.r0[0] + p.tile_rows, rm.RG);
   u.kvh = rm.pool_rows ? 0 : u.g / rm.kv_div;
   u.ph = rm.pool_rows ? u.g : u.kvh % a.Hk;
   const int b = rm.pool_rows ? 0 : u.kvh / a.Hk;
-  u.kl = key_list(a, rm, b, u.r0[0], r1);
+  u.kl = key_list(a, rm, b, k0, k1);
   u.hi = u.kl.lo + (u.kl.total - u.kl.np - u.kl.ns);
   u.tp = (u.kl.np + KT - 1) / KT;
   u.ts = (u.kl.ns + KT - 1) / KT;
@@ -126,7 +134,7 @@ __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& 
   const int ntile = u.tp + u.ts + to;
   u.t0 = (int)((int64_t)ntile * u.sp / p.out.nsplit);
   const int t1 = (int)((int64_t)ntile * (u.sp + 1) / p.out.nsplit);
-  u.nt = t1 - u.t0;
+  u.nt = u.r0[0] < r1 ? t1 - u.t0 : 0;           // 0: the second half of a unit with one row tile
   u.safe_lo = u.safe_hi = 0;
   if (!rm.pool_rows && rm.use_own) {
     const int len = cache_len(a, b);
@@ -136,7 +144,7 @@ __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& 
   }
   for (int t = 0; t < 2; ++t) {
     u.lead[t] = u.oa[t] = u.ob[t] = 0;
-    const int ra = u.r0[t], rz = t == 0 ? u.r0[1] : r1;
+    const int ra = u.r0[t], rz = t == 0 ? min(u.r0[1], r1) : r1;
     if (ra >= rz) continue;                      // no rows
     u.lead[t] = u.oa[t] = u.ob[t] = max(0, min(u.nt, u.tp + u.ts - u.t0));
     if (to == 0) continue;

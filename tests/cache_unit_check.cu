@@ -20,8 +20,12 @@ static int check(const CacheArgs& a, const CacheRows& rm, int nsplit) {
   const int unit_rows = TILES * p.tile_rows;
   p.nrb = (rm.RG + unit_rows - 1) / unit_rows;
   p.units = rm.groups * p.nrb * nsplit;
-  for (int heavy = 0; heavy < 2; ++heavy) {
-    p.heavy_first = heavy;
+  const int whole = p.units;
+  // in either order, with no unit, the last two and every unit in halves
+  for (int turn = 0; turn < (TILES == 2 ? 6 : 2); ++turn) {
+    p.heavy_first = turn % 2;
+    p.halved = turn / 2 == 0 ? 0 : turn / 2 == 1 ? std::min(whole, 2) : whole;
+    p.units = whole + p.halved;
     // per row of q: how often each key was met (prefix, then own)
     const int rows = a.B * a.H * a.Nq, keys = a.P + a.S;
     std::vector<unsigned char> met((size_t)rows * keys, 0), touched(rows, 0);
