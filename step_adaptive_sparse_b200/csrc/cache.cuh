@@ -8,8 +8,8 @@
 //   * of the sequence's own keys, j <= p (causal) or j < len, and with a
 //     window only j > p - window or j < sinks.
 // A split of the keys over several CTAs leaves per split and row the running
-// maximum m (log2 units), the sum l and the unnormalised output; join.cu adds
-// them up.
+// maximum m (log2 units), the sum l and the unnormalised output; cache_join.cu
+// adds them up.
 #pragma once
 
 #include <limits.h>
