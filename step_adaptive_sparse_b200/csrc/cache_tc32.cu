@@ -187,7 +187,7 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma) : "memory");
     // -------------------------------------------------------------- products
     if (warp == kReadWarps) {
-      uint32_t unit_count = 0;
+      uint32_t unit_count = 0, q_count = 0;
       uint32_t s_it = 0, p_it = 0;     // tiles whose scores, whose outputs have been issued
       bool ok = true;
       const uint64_t dk = sdesc(sbase, 16, 1024), dv = sdesc(sbase + G::kSmemV, G::kHalf, 1024);
@@ -247,14 +247,17 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         if (lane == 0) mbar_arrive(bar(BAR_REC_EMPTY + slot));
         __syncwarp();
         if (!valid) break;
-        if (!(ok = warp_wait_all(bar(BAR_Q_FULL), unit_count & 1u, abort_flag))) break;
+        ++unit_count;
+        // Units without a tile have no queries.  Those of the next unit that has
+        // some are written after the scores of the last one's tiles, which follow
+        // this wait, so that no phase of the barrier passes unseen.
+        if (nt == 0) continue;
+        if (!(ok = warp_wait_all(bar(BAR_Q_FULL), q_count++ & 1u, abort_flag))) break;
         for (int j = 0; j < nt; ++j) {
           if (j == 0 && !(ok = qk())) break;
           if (j + 1 < nt && !(ok = qk())) break;
           if (!(ok = pv())) break;
         }
-        if (!ok) break;
-        ++unit_count;
       }
       int drain_abort = 0;
       if (elect_one()) mma_commit(bar(BAR_DRAIN));
@@ -294,10 +297,11 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
       // this thread's row and what it sees; rows that do not exist see all
       const int r = u.r0[0] + trow;
       const bool rvalid = r < prm.rm.RG;
+      const int nt = u.nt;
       // The query's parts, once the last unit's scores are done with the old ones
       // (the last of them was waited for).  The span is kept in shared memory:
       // the output and a score row fill the registers.
-      {
+      if (nt > 0) {
         KeySpan sp{0, INT_MAX};
         const float* q = nullptr;
         if (rvalid) {
@@ -323,7 +327,6 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         tc_fence_before();
         mbar_arrive(bar(BAR_Q_FULL));
       }
-      const int nt = u.nt;
       float m = -INFINITY, l = 0.f, o[D];
 #pragma unroll
       for (int i = 0; i < D; ++i) o[i] = 0.f;

@@ -732,3 +732,31 @@ def test_long_cache_offsets_past_32_bits():
     host = [x.double().numpy() for x in (q, kt, vt)] + [np.zeros((Hk, 0, D))] * 2
     want, _, size = co.cache_attention(*host[:3], [tail] * B, 0.1)
     close(o, want, bound(host, want, size, "bf16", 0.1, tail))
+
+
+@pytest.mark.parametrize("B,H,Hk,Nq,S,D,P,lens", [
+    # runs of sequences without a token: several units of a block in a row have no tile
+    (64, 16, 16, 130, 260, 64, 0, [0] * 20 + [260] + [0] * 20 + [131, 1] + [0] * 21),
+    (60, 24, 24, 129, 200, 128, 65, [0] * 30 + [200, 3] + [0] * 28),
+    # splits of a long cache that holds few tokens
+    (2, 2, 1, 70, 30000, 64, 0, [90, 0]),
+])
+def test_units_without_tiles_in_fp32(B, H, Hk, Nq, S, D, P, lens):
+    dev, host, dl = make(101, "f32", B, H, Hk, Nq, S, D, lens, P=P)
+    scale = D ** -0.5
+    o = Guarded((B, H, Nq, D), torch.float32, NAN)
+    some = [b for b in range(B) if lens[b] > 0]
+    none = [b for b in range(B) if lens[b] == 0]
+    top = max(lens)                            # (the oracle does without the cache's empty end)
+    few = [host[0][some], host[1][some][:, :, :top], host[2][some][:, :, :top], host[3], host[4]]
+    runs = [(lambda: run_sink(dev, dl, "f32", 100, 2, scale, o.t), dict(window=100, sinks=2))]
+    if P:
+        runs.append((lambda: run_prefix(dev, dl, "f32", 1, scale, o.t), dict(kp=host[3], vp=host[4])))
+    for run, kw in runs:
+        o.t.fill_(NAN)
+        run()
+        want, _, size = co.cache_attention(*few[:3], [lens[b] for b in some], scale, **kw)
+        close(o.t[some], want, bound(few, want, size, "f32", scale, top + P))
+        assert (o.t[none] == 0).all()
+        o.check()
+    assert area.area_kernel_error() == 0
