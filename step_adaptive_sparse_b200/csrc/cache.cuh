@@ -259,6 +259,12 @@ struct EvictArgs {
   int *lenso, *idx;
   int B, Hk, S, So, D, budget, sinks, recent, elem;   // elem: bytes of a value
 };
+// Where part `part` of n things begins when `parts` parts share them evenly.  (Parts
+// are walked from here to the next one's, which no 32-bit index leaves: S and So end
+// 4096 before the largest.)
+__host__ __device__ __forceinline__ int share_of(int n, int part, int parts) {
+  return (int)((int64_t)n * part / parts);
+}
 cudaError_t launch_cache_evict(const EvictArgs& e, cudaStream_t s);
 
 }  // namespace area

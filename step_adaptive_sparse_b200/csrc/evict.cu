@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs e, int 
   const float* acc = e.acc + g * e.S;
   int* idx = e.idx + g * e.So;
   float* acco = e.acco + g * e.So;
-  auto share = [&](int of, int r) { return (int)((int64_t)of * r / cs); };
+  auto share = [&](int of, int r) { return share_of(of, r, cs); };
   if (g % e.Hk == 0 && rank == 0 && tid == 0) e.lenso[b] = kept;
   for (int j = kept + share(e.So - kept, rank) + tid; j < kept + share(e.So - kept, rank + 1);
        j += kThreads) {
@@ -274,10 +274,10 @@ __global__ void __launch_bounds__(kThreads) evict_copy_kernel(const EvictArgs e,
   const int blk = blockIdx.x % blocks_per_head;
   const int m = min(evict_len(e, (int)(g / e.Hk)), e.budget);
   const int* idx = e.idx + g * e.So;
-  const int r0 = (int)((int64_t)m * blk / blocks_per_head);
-  const int r1 = (int)((int64_t)m * (blk + 1) / blocks_per_head);
+  const int r0 = share_of(m, blk, blocks_per_head), r1 = share_of(m, blk + 1, blocks_per_head);
   copy_rows(e, g, r1 - r0, [&](int i) { return make_int2(idx[r0 + i], r0 + i); });
-  for (int j = blk * kThreads + threadIdx.x; j < e.So; j += blocks_per_head * kThreads)
+  const int j1 = share_of(e.So, blk + 1, blocks_per_head);
+  for (int j = share_of(e.So, blk, blocks_per_head) + threadIdx.x; j < j1; j += kThreads)
     e.acco[g * e.So + j] = j < m ? e.acc[g * e.S + idx[j]] : 0.f;
 }
 

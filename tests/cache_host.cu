@@ -1,0 +1,39 @@
+// The host side of the key/value cache's calls without a GPU: their entry points
+// (cache_api.cu) over launches that only count themselves, and the index
+// arithmetic that kernels share with the host.  Built as a shared library and
+// called by CPU tests; no kernel is in it, so that a call that passes validation
+// touches no memory.
+#include "cache_api.cu"
+
+extern "C" {
+int host_share_of(int n, int part, int parts) { return area::share_of(n, part, parts); }
+}
+
+namespace {
+int g_launches = 0;
+cudaError_t counted() {
+  ++g_launches;
+  return cudaSuccess;
+}
+}  // namespace
+
+extern "C" int host_launches(void) {        // since the last look
+  const int n = g_launches;
+  g_launches = 0;
+  return n;
+}
+
+namespace area {
+int fail_cuda(cudaError_t) { return AREA_ECUDA; }
+cudaError_t launch_cache_dec_bf16(const CacheArgs&, const CacheRows&, const CacheOut&, cudaStream_t) { return counted(); }
+cudaError_t launch_cache_dec_f32(const CacheArgs&, const CacheRows&, const CacheOut&, cudaStream_t) { return counted(); }
+cudaError_t launch_cache_tc(const CacheArgs&, const CacheRows&, const CacheOut&, cudaStream_t) { return counted(); }
+cudaError_t launch_cache_tc32(const CacheArgs&, const CacheRows&, const CacheOut&, cudaStream_t) { return counted(); }
+cudaError_t launch_cache_join(const CacheArgs&, const float*, const float2*, int, int64_t, float*, int,
+                              cudaStream_t) { return counted(); }
+cudaError_t launch_cache_join_weights(const CacheArgs&, const CacheOut&, int, int, cudaStream_t) { return counted(); }
+cudaError_t launch_cache_weights_tc(const CacheArgs&, const float*, const float*, float*, int, cudaStream_t) {
+  return counted();
+}
+cudaError_t launch_cache_evict(const EvictArgs&, cudaStream_t) { return counted(); }
+}  // namespace area
