@@ -65,7 +65,7 @@ struct CacheOut {
 };
 
 __host__ __device__ __forceinline__ int cache_len(const CacheArgs& a, int b) {
-  if (!a.lens) return a.S;
+  if (!a.lens || a.S == 0) return a.S;       // without room for tokens lengths are not read
   const int n = a.lens[b];
   return n < 0 ? 0 : n > a.S ? a.S : n;      // a length outside the cache is cut to it
 }

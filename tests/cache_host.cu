@@ -6,6 +6,12 @@
 #include "cache_api.cu"
 
 extern "C" {
+int host_cache_len(const int* lens, int S, int b) {
+  area::CacheArgs a{};
+  a.lens = lens;
+  a.S = S;
+  return area::cache_len(a, b);
+}
 int host_share_of(int n, int part, int parts) { return area::share_of(n, part, parts); }
 }
 

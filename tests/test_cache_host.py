@@ -37,3 +37,25 @@ def test_shares_follow_one_another_and_stay_within_32_bits(host, n, parts):
         a, b = host.host_share_of(n, p, parts), host.host_share_of(n, p + 1, parts)
         assert a == n * p // parts and b == n * (p + 1) // parts
         assert max(a + 255, b - 1 + 256) <= INT_MAX
+
+
+# ---- lengths ---------------------------------------------------------------------------------
+
+def test_lengths_are_read_only_where_there_is_room_for_tokens(host):
+    """The kernels' own reading of a length, whatever the entry point has done before.  (A page
+    that may not be read: a process that reads it ends, so a child process looks first.)"""
+    import sys
+    look = ("import ctypes, mmap\n"
+            "libc = ctypes.CDLL(None)\n"
+            "libc.mmap.restype = ctypes.c_void_p\n"
+            "page = libc.mmap(None, 4096, 0, mmap.MAP_PRIVATE | mmap.MAP_ANONYMOUS, -1, 0)\n"
+            f"h = ctypes.CDLL({host._name!r})\n"
+            "h.host_cache_len.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int]\n"
+            "print(h.host_cache_len(page, 0, 1))\n")
+    r = subprocess.run([sys.executable, "-c", look], capture_output=True, text=True)
+    assert (r.returncode, r.stdout) == (0, "0\n")
+    host.host_cache_len.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int]
+    lens = (ctypes.c_int * 5)(7, 0, -3, 100, -INT_MAX - 1)
+    at = ctypes.addressof(lens)
+    assert [host.host_cache_len(at, 9, b) for b in range(5)] == [7, 0, 0, 9, 0]
+    assert host.host_cache_len(None, 9, 3) == 9
