@@ -8,6 +8,8 @@ import subprocess
 import pytest
 
 INT_MAX = 2 ** 31 - 1
+OK, EINVAL, EUNSUPPORTED, ENOSPACE = 0, 1, 2, 3
+CALLS = ["area_sink_attn", "area_prefix_attn", "area_cache_attn", "area_cache_evict"]
 
 
 @pytest.fixture(scope="session")
@@ -21,7 +23,11 @@ def host(tmp_path_factory):
     subprocess.run([nvcc, "-O1", "-std=c++17", "-Wno-deprecated-gpu-targets", "-shared", "-Xcompiler", "-fPIC",
                     "-Xlinker", "-Bsymbolic", "-I", os.path.join(root, "include"), "-I", b.CSRC,
                     os.path.join(root, "tests", "cache_host.cu"), "-o", out], check=True)
-    return ctypes.CDLL(out)
+    lib = ctypes.CDLL(out)
+    from step_adaptive_sparse_b200 import binding
+    for name in CALLS + [c + "_ws_bytes" for c in CALLS[:3]]:
+        getattr(lib, name).restype, getattr(lib, name).argtypes = binding._SIGS[name]
+    return lib
 
 
 # ---- how eviction shares the weights behind the kept tokens out ------------------------------
@@ -59,3 +65,136 @@ def test_lengths_are_read_only_where_there_is_room_for_tokens(host):
     at = ctypes.addressof(lens)
     assert [host.host_cache_len(at, 9, b) for b in range(5)] == [7, 0, 0, 9, 0]
     assert host.host_cache_len(None, 9, 3) == 9
+
+
+# ---- what the calls accept and refuse ---------------------------------------------------------
+
+FAR = 1 << 40
+BUFFERS = ["q", "kp", "vp", "k", "v", "lens", "acc", "o", "acco", "ws", "ko", "vo", "lenso", "idx"]
+AT = {n: (i + 1) * FAR for i, n in enumerate(BUFFERS)}            # every buffer on its own
+SIZES = {"B": 2, "H": 4, "Hk": 2, "Nq": 5, "P": 40, "S": 9000, "D": 64, "window": 6000, "sinks": 3}
+ARGS = {
+    "sink": "q k v lens o ws nb B H Hk Nq S D window sinks scale dtype stream",
+    "prefix": "q kp vp k v lens o ws nb B H Hk Nq P S D causal scale dtype stream",
+    "cache": "q k v lens acc o acco ws nb B H Hk Nq S D scale dtype stream",
+    "evict": "k v acc lens ko vo acco lenso idx B Hk S So D budget sinks recent dtype stream",
+}
+EVICT = {"So": 3000, "budget": 2000, "sinks": 4, "recent": 100}
+
+
+def given(op, dtype=1, **change):
+    """A call's arguments: every buffer at an address of its own, unless `change` moves it."""
+    a = {**AT, **SIZES, "dtype": dtype, "causal": 1, "scale": 0.125, "stream": 0, "nb": 1 << 36}
+    if op == "evict":
+        a.update(EVICT)
+    a.update(change)
+    return a
+
+
+def ask(host, op, **kw):
+    """The call's status.  Refused calls launch nothing, accepted ones something."""
+    a = given(op, **kw)
+    host.host_launches()
+    status = getattr(host, "area_cache_evict" if op == "evict" else f"area_{op}_attn")(
+        *[a[n] for n in ARGS[op].split()])
+    assert (host.host_launches() > 0) == (status == OK)
+    return status
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("op,change", [(op, {}) for op in ARGS] + [
+    ("sink", {"lens": None}), ("sink", {"window": 1, "sinks": 0}), ("sink", {"window": INT_MAX, "sinks": INT_MAX}),
+    ("sink", {"Nq": 9500}), ("sink", {"S": 1}), ("sink", {"Hk": 4}), ("sink", {"Hk": 1}), ("sink", {"D": 128}),
+    ("sink", {"scale": 1e-30}), ("sink", {"scale": 1e38}), ("sink", {"stream": None}),
+    ("sink", {"S": 100, "window": 50, "nb": 0, "ws": None}),
+    ("prefix", {"causal": 0}), ("prefix", {"P": 0, "kp": None, "vp": None}),
+    ("prefix", {"S": 0, "k": None, "v": None}), ("prefix", {"S": 0, "lens": AT["o"]}),
+    ("cache", {"acc": None}), ("cache", {"acc": AT["acco"]}), ("cache", {"lens": None}), ("cache", {"Nq": 300}),
+    ("evict", {"lens": None}), ("evict", {"budget": 1, "sinks": 0, "recent": 0}), ("evict", {"budget": 104}),
+    ("evict", {"So": 2000}), ("evict", {"So": 12000, "budget": 9500}),
+    ("evict", {"So": 9000, "ko": AT["k"], "vo": AT["v"], "acco": AT["acc"]})])
+def test_accepted(host, op, change, dtype):
+    """The calls that the refusals below change in one place each."""
+    assert ask(host, op, dtype=dtype, **change) == OK
+
+
+ATTN = ([{n: None} for n in ("q", "o", "k", "v", "ws")] +
+        [{n: AT[n] + 8} for n in ("q", "k", "v")] + [{"o": AT["o"] + 16}, {"ws": AT["ws"] + 16}] +
+        [{"lens": AT["lens"] + 2}] + [{n: 0} for n in ("B", "H", "Hk", "Nq")] + [{n: -1} for n in ("B", "H", "Hk", "Nq", "S")] +
+        [{"Hk": 3}, {"Hk": 8}] + [{"scale": x} for x in (0.0, -0.125, float("nan"), float("inf"), -float("inf"))])
+REFUSED = (
+    [(op, c, EINVAL) for op in ("sink", "prefix", "cache") for c in ATTN] +
+    [(op, c, EUNSUPPORTED) for op in ("sink", "prefix", "cache") for c in
+     ({"D": 0}, {"D": 96}, {"D": 256}, {"dtype": 2}, {"dtype": -1}, {"S": INT_MAX},
+      {"B": INT_MAX, "H": INT_MAX, "Hk": 1, "Nq": INT_MAX}, {"B": 1 << 20, "H": 1 << 10, "Hk": 1 << 10, "Nq": 2})] +
+    [(op, {"nb": 0}, ENOSPACE) for op in ("sink", "prefix", "cache")] +
+    [("sink", c, EINVAL) for c in ({"window": 0}, {"window": -1}, {"sinks": -1}, {"S": 0})] +
+    [("prefix", c, EINVAL) for c in ({"kp": None}, {"vp": None}, {"kp": AT["kp"] + 8}, {"vp": AT["vp"] + 4}, {"P": -1},
+                                     {"P": 0, "S": 0}, {"causal": 2}, {"causal": -1})] +
+    [("prefix", {"P": 1 << 30, "S": 1 << 30}, EUNSUPPORTED)] +
+    [("cache", c, EINVAL) for c in ({"acco": None}, {"acco": AT["acco"] + 2}, {"acc": AT["acc"] + 1}, {"S": 0})] +
+    [("evict", {n: None}, EINVAL) for n in ("k", "v", "acc", "ko", "vo", "acco", "lenso", "idx")] +
+    [("evict", {n: AT[n] + 8}, EINVAL) for n in ("k", "v", "ko", "vo")] +
+    [("evict", {n: AT[n] + 2}, EINVAL) for n in ("acc", "lens", "acco", "lenso", "idx")] +
+    [("evict", {n: x}, EINVAL) for n in ("B", "Hk", "S", "So", "budget") for x in (0, -1)] +
+    [("evict", c, EINVAL) for c in ({"budget": 0, "sinks": 0, "recent": 0}, {"sinks": -1}, {"recent": -1}, {"sinks": 1901}, {"budget": 3001},
+                                    {"sinks": INT_MAX, "recent": INT_MAX})] +
+    [("evict", c, EUNSUPPORTED) for c in ({"dtype": 2}, {"D": 80}, {"S": INT_MAX}, {"So": INT_MAX},
+                                          {"B": 1 << 16, "Hk": 1 << 16})])
+
+
+@pytest.mark.parametrize("op,change,status", REFUSED)
+def test_refused_for_one_change(host, op, change, status):
+    assert ask(host, op, **change) == status
+
+
+@pytest.mark.parametrize("op", ["sink", "prefix", "cache"])
+def test_a_workspace_of_the_size_asked_for_is_accepted_and_one_byte_less_refused(host, op):
+    a = given(op)
+    need = ctypes.c_size_t()
+    names = [n for n in ARGS[op].split() if n in SIZES or n == "dtype"]
+    assert getattr(host, f"area_{op}_attn_ws_bytes")(*[a[n] for n in names], ctypes.byref(need)) == OK
+    assert need.value > 0 and getattr(host, f"area_{op}_attn_ws_bytes")(*[a[n] for n in names], None) == EINVAL
+    assert ask(host, op, nb=need.value) == OK
+    assert ask(host, op, nb=need.value - 1) == ENOSPACE
+
+
+def bytes_of(host, op):
+    a = given(op)
+    e, kv = 2, a["B"] * a["Hk"] * a["D"] * 2
+    n = {"q": a["B"] * a["H"] * a["Nq"] * a["D"] * e, "k": kv * a["S"], "v": kv * a["S"],
+         "kp": a["Hk"] * a["P"] * a["D"] * e, "vp": a["Hk"] * a["P"] * a["D"] * e, "lens": a["B"] * 4,
+         "acc": a["B"] * a["Hk"] * a["S"] * 4}
+    n["o"], n["acco"] = n["q"], n["acc"]
+    if op == "evict":
+        out = a["B"] * a["Hk"] * a["So"]
+        n.update(ko=out * a["D"] * e, vo=out * a["D"] * e, acco=out * 4, idx=out * 4, lenso=a["B"] * 4)
+        return n
+    need = ctypes.c_size_t()
+    names = [x for x in ARGS[op].split() if x in SIZES or x == "dtype"]
+    getattr(host, f"area_{op}_attn_ws_bytes")(*[a[x] for x in names], ctypes.byref(need))
+    n["ws"] = need.value
+    return n
+
+
+@pytest.mark.parametrize("op", list(ARGS))
+def test_overlaps_are_refused_and_neighbours_are_not(host, op):
+    """Every output against every input and every other output: at its first and its last bytes,
+    and just before and just behind it."""
+    size = bytes_of(host, op)
+    have = [n for n in ARGS[op].split() if n in AT]
+    outs = {"o", "acco", "ws", "ko", "vo", "lenso", "idx"}
+    step = {"o": 32, "ws": 32, "lens": 4, "lenso": 4, "acc": 4, "acco": 4, "idx": 4}      # alignments
+    kw = {"nb": size["ws"]} if "ws" in size else {}
+    for x in [n for n in have if n in outs]:
+        for y in [n for n in have if n != x]:
+            # the one of the two that may lie anywhere the other ends is moved
+            mv, st = (x, y) if step.get(x, 16) <= step.get(y, 16) else (y, x)
+            al = step.get(mv, 16)
+            inside = (size[st] - 1) // al * al
+            for at in (AT[st] + inside, AT[st] - size[mv] + al if size[mv] > al else AT[st]):
+                assert ask(host, op, **{mv: at}, **kw) == EINVAL, (mv, "over", st, at - AT[st])
+            if not (op == "cache" and {x, y} == {"acc", "acco"}):
+                assert ask(host, op, **{mv: AT[st]}, **kw) == EINVAL, (mv, "on", st)
+            for at in (AT[st] + -(-size[st] // al) * al, AT[st] - -(-size[mv] // al) * al):
+                assert ask(host, op, **{mv: at}, **kw) == OK, (mv, "beside", st, at - AT[st])
