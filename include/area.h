@@ -482,7 +482,8 @@ int area_window_attn_noalloc(const void* q, const void* k, const void* v,
  *     acc (area_cache_attn).
  *   - Sums run in a fixed order: outputs are bit-identical from run to run
  *     and in CUDA-graph replays.
- *   - scale is positive.  dtype: bf16 or fp32; D: 64 or 128.
+ *   - scale is positive, and finite also times log2(e).  dtype: bf16 or fp32;
+ *     D: 64 or 128.
  * Errors of all of them: AREA_EINVAL (null, bad size, misaligned or
  * overlapping buffer), AREA_EUNSUPPORTED (dtype, D, or sizes past 32-bit row
  * indexes: B * H * Nq, P + S above 2^31 - 257), AREA_ENOSPACE, AREA_ECUDA.

@@ -236,7 +236,8 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
   const int st = cache_plan(op, a.B, a.H, a.Hk, a.Nq, a.P, a.S, a.D, a.window, a.sinks, dtype, &p);
   if (st != AREA_OK) return st;
   if ((a.S > 0 && (!a.k || !a.v)) || (a.P > 0 && (!a.kp || !a.vp))) return AREA_EINVAL;
-  if (!(scale > 0.f) || !isfinite(scale)) return AREA_EINVAL;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.f) || !isfinite(a.scale_log2)) return AREA_EINVAL;
   if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.kp, 16) ||
       !aligned(a.vp, 16) || !aligned(a.o, 32) || !aligned(a.lens, 4))
     return AREA_EINVAL;
@@ -255,7 +256,6 @@ int cache_call(int op, CacheArgs& a, float scale, const float* acc, float* acco,
     for (int j = 0; j < i; ++j)
       if (overlap(to[i], to[j])) return AREA_EINVAL;
   }
-  a.scale_log2 = scale * 1.4426950408889634f;
   char* w = static_cast<char*>(ws);
   CacheOut out{};
   out.direct = p.slots == 0;

@@ -120,8 +120,9 @@ def test_accepted(host, op, change, dtype):
 
 ATTN = ([{n: None} for n in ("q", "o", "k", "v", "ws")] +
         [{n: AT[n] + 8} for n in ("q", "k", "v")] + [{"o": AT["o"] + 16}, {"ws": AT["ws"] + 16}] +
-        [{"lens": AT["lens"] + 2}] + [{n: 0} for n in ("B", "H", "Hk", "Nq")] + [{n: -1} for n in ("B", "H", "Hk", "Nq", "S")] +
-        [{"Hk": 3}, {"Hk": 8}] + [{"scale": x} for x in (0.0, -0.125, float("nan"), float("inf"), -float("inf"))])
+        [{"lens": AT["lens"] + 2}] + [{n: 0} for n in ("B", "H", "Hk", "Nq")] +
+        [{n: -1} for n in ("B", "H", "Hk", "Nq", "S")] +
+        [{"Hk": 3}, {"Hk": 8}] + [{"scale": x} for x in (0.0, -0.125, float("nan"), float("inf"), -float("inf"), 2.4e38)])
 REFUSED = (
     [(op, c, EINVAL) for op in ("sink", "prefix", "cache") for c in ATTN] +
     [(op, c, EUNSUPPORTED) for op in ("sink", "prefix", "cache") for c in
@@ -137,8 +138,8 @@ REFUSED = (
     [("evict", {n: AT[n] + 8}, EINVAL) for n in ("k", "v", "ko", "vo")] +
     [("evict", {n: AT[n] + 2}, EINVAL) for n in ("acc", "lens", "acco", "lenso", "idx")] +
     [("evict", {n: x}, EINVAL) for n in ("B", "Hk", "S", "So", "budget") for x in (0, -1)] +
-    [("evict", c, EINVAL) for c in ({"budget": 0, "sinks": 0, "recent": 0}, {"sinks": -1}, {"recent": -1}, {"sinks": 1901}, {"budget": 3001},
-                                    {"sinks": INT_MAX, "recent": INT_MAX})] +
+    [("evict", c, EINVAL) for c in ({"budget": 0, "sinks": 0, "recent": 0}, {"sinks": -1}, {"recent": -1},
+                                    {"sinks": 1901}, {"budget": 3001}, {"sinks": INT_MAX, "recent": INT_MAX})] +
     [("evict", c, EUNSUPPORTED) for c in ({"dtype": 2}, {"D": 80}, {"S": INT_MAX}, {"So": INT_MAX},
                                           {"B": 1 << 16, "Hk": 1 << 16})])
 
