@@ -9,7 +9,7 @@ namespace {
 
 constexpr int64_t kSms = 148;        // B200; the workspace's size may not hang on the device
 
-constexpr int64_t kPoolBytes = 32 << 20;
+constexpr double kPoolBytes = 32 << 20;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t ceil256(int64_t n) { return (n + 255) & ~int64_t(255); }
@@ -186,7 +186,7 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   // Few rows of a sequence: the prefix against the rows of all sequences, once
   // it is so large that reading it from L2 for each costs more than the second
   // launch and the join.
-  const int64_t pre = (int64_t)B * Hk * P * D * (dtype == AREA_DTYPE_BF16 ? 4 : 8);
+  const double pre = (double)B * Hk * P * D * (dtype == AREA_DTYPE_BF16 ? 4 : 8);
   const bool pool = op == CACHE_OP_PREFIX && P > 0 && B > 1 && R < 64 && pre > kPoolBytes;
   p->pooled = CacheLaunch{};
   CacheLaunch& m = p->main;

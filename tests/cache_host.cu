@@ -12,6 +12,12 @@ int host_cache_len(const int* lens, int S, int b) {
   a.S = S;
   return area::cache_len(a, b);
 }
+// 1: the prefix goes against the rows of all sequences in a launch of its own.
+int host_pools(int B, int H, int Hk, int Nq, int P, int S, int D, int dtype) {
+  area::CachePlan p;
+  if (area::cache_plan(area::CACHE_OP_PREFIX, B, H, Hk, Nq, P, S, D, INT_MAX, 0, dtype, &p) != AREA_OK) return -1;
+  return p.pooled.used;
+}
 int host_share_of(int n, int part, int parts) { return area::share_of(n, part, parts); }
 }
 

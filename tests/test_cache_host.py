@@ -199,3 +199,13 @@ def test_overlaps_are_refused_and_neighbours_are_not(host, op):
                 assert ask(host, op, **{mv: AT[st]}, **kw) == EINVAL, (mv, "on", st)
             for at in (AT[st] + -(-size[st] // al) * al, AT[st] - -(-size[mv] // al) * al):
                 assert ask(host, op, **{mv: at}, **kw) == OK, (mv, "beside", st, at - AT[st])
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("B,H,Hk,Nq,P,S,pools", [
+    (64, 32, 8, 1, 30000, 100, 1), (1, 32, 8, 1, 30000, 100, 0), (64, 32, 8, 1, 64, 100, 0),
+    (1 << 20, 8, 8, 1, 1 << 20, 1, 1),
+    # the bytes that all sequences would read of the prefix pass 2^63 and 2^64
+    (1 << 29, 1, 1, 1, 1 << 28, 1, 1), (1 << 30, 1, 1, 1, 1 << 30, 0, 1), (1 << 28, 4, 4, 1, 3 << 28, 1, 1)])
+def test_long_prefixes_of_large_batches_are_read_once(host, B, H, Hk, Nq, P, S, pools, dtype):
+    assert host.host_pools(B, H, Hk, Nq, P, S, 128, dtype) == pools
