@@ -177,11 +177,12 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   if (H % Hk || window < 1 || sinks < 0) return AREA_EINVAL;
   if (S < 1 && P < 1) return AREA_EINVAL;
   if (D != 64 && D != 128) return AREA_EUNSUPPORTED;
-  // row and key indexes are 32-bit, a key list may hold prefix and cache
+  // row and key indexes are 32-bit, also rounded up to a block; a key list may hold
+  // prefix and cache
   if ((int64_t)P + S > INT_MAX - 256) return AREA_EUNSUPPORTED;
   if ((int64_t)B * H > INT_MAX) return AREA_EUNSUPPORTED;
   p->rows = (int64_t)B * H * Nq;
-  if (p->rows > INT_MAX) return AREA_EUNSUPPORTED;
+  if (p->rows > INT_MAX - 256) return AREA_EUNSUPPORTED;
   const int R = H / Hk * Nq;
   // Few rows of a sequence: the prefix against the rows of all sequences, once
   // it is so large that reading it from L2 for each costs more than the second

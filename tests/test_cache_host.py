@@ -209,3 +209,16 @@ def test_overlaps_are_refused_and_neighbours_are_not(host, op):
     (1 << 29, 1, 1, 1, 1 << 28, 1, 1), (1 << 30, 1, 1, 1, 1 << 30, 0, 1), (1 << 28, 4, 4, 1, 3 << 28, 1, 1)])
 def test_long_prefixes_of_large_batches_are_read_once(host, B, H, Hk, Nq, P, S, pools, dtype):
     assert host.host_pools(B, H, Hk, Nq, P, S, 128, dtype) == pools
+
+
+def test_row_and_key_indexes_end_where_the_header_says(host):
+    """B * H * Nq and P + S up to 2^31 - 257: kernels round both up to their blocks in 32 bits."""
+    need, top = ctypes.c_size_t(), 2 ** 31 - 257
+    for dtype in (0, 1):
+        for D in (64, 128):
+            for by, want in ((0, OK), (1, EUNSUPPORTED), (256, EUNSUPPORTED)):
+                at = ctypes.byref(need)
+                assert host.area_sink_attn_ws_bytes(1, 1, 1, top + by, 10, D, 5, 0, dtype, at) == want
+                assert host.area_prefix_attn_ws_bytes(1, 1, 1, top + by, 10, 10, D, dtype, at) == want
+                assert host.area_prefix_attn_ws_bytes(1, 1, 1, 1, 7, top + by - 7, D, dtype, at) == want
+                assert host.area_sink_attn_ws_bytes(1, 1, 1, 1, top + by, D, 5, 0, dtype, at) == want
