@@ -18,6 +18,7 @@ import numpy as np
 import pytest
 import torch
 
+import cache_bounds as cb
 import step_adaptive_sparse_b200 as area
 from oracle import cache_oracle as co
 
@@ -760,3 +761,44 @@ def test_units_without_tiles_in_fp32(B, H, Hk, Nq, S, D, P, lens):
         assert (o.t[none] == 0).all()
         o.check()
     assert area.area_kernel_error() == 0
+
+
+# ---- fp32 is held to fp32: a bound that inputs of 16 significand bits leave (cache_bounds.py) ----
+
+def fp32_case(case):
+    B, H, Hk, Nq, P, S, D, window, sinks, lens = case
+    x = cb.inputs(111, B, H, Hk, Nq, P, S, D)
+    return x, [torch.from_numpy(y).cuda() for y in x], torch.tensor(lens, dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("case", cb.SINK)
+def test_fp32_window_attention_keeps_fp32(case):
+    B, H, Hk, Nq, P, S, D, window, sinks, lens = case
+    x, dev, dl = fp32_case(case)
+    o = torch.full_like(dev[0], NAN)
+    run_sink(dev, dl, "f32", window, sinks, cb.SCALE, o)
+    want, tol, _, _ = cb.call(*x[:3], lens, cb.SCALE, lambda n: co.visible(n, Nq, S, window, sinks))
+    close(o, want, tol)
+
+
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("case", cb.PREFIX)
+def test_fp32_prefix_attention_keeps_fp32(case, causal):
+    B, H, Hk, Nq, P, S, D, window, sinks, lens = case
+    x, dev, dl = fp32_case(case)
+    o = torch.full_like(dev[0], NAN)
+    run_prefix(dev, dl, "f32", causal, cb.SCALE, o)
+    want, tol, _, _ = cb.call(*x[:3], lens, cb.SCALE, lambda n: co.visible(n, Nq, S, causal=bool(causal)),
+                              kp=x[3], vp=x[4], causal=bool(causal))
+    close(o, want, tol)
+
+
+@pytest.mark.parametrize("case", cb.CACHE)
+def test_fp32_weights_keep_fp32(case):
+    B, H, Hk, Nq, P, S, D, window, sinks, lens = case
+    x, dev, dl = fp32_case(case)
+    o, acco = torch.full_like(dev[0], NAN), torch.full((B, Hk, S), NAN, device="cuda")
+    run_cache(dev, dl, "f32", cb.SCALE, None, o, acco)
+    want, tol, got, wtol = cb.call(*x[:3], lens, cb.SCALE, lambda n: co.visible(n, Nq, S))
+    close(o, want, tol)
+    close(acco, got, wtol)
