@@ -363,6 +363,7 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
       uint32_t whole = 0;                      // of 32 tiles, one bit each
       int at32 = INT_MIN / 2;                  // the first of them
       float m = -INFINITY, l = 0.f;
+      RowRef ref{sl2, 0.f};                    // nothing seen so far: all weights 0
       for (int j = first; j <= last;) {
         if (j - at32 >= 32) {
           at32 = j;
@@ -417,17 +418,19 @@ cache_tc_kernel(const __grid_constant__ Maps tm, const __grid_constant__ UnitPar
         const bool rescale =
             j > first && __any_sync(0xffffffffu, rvalid && mnew > m + kRescaleThreshold);
         const float alpha = rescale ? (m == -INFINITY ? 0.f : fast_exp2(m - mnew)) : 1.f;
-        if (j == first || rescale) m = mnew;
+        if (j == first || rescale) {
+          if (mnew > m) ref = row_ref(pm[0], mnew, sl2);
+          m = mnew;
+        }
         l *= alpha;
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
-        const float negm = m == -INFINITY ? 0.f : -m;     // nothing seen so far: all weights 0
 #pragma unroll
         for (int h = 0; h < kPParts; ++h) {
           constexpr int kKeys = 128 / kPParts;
 #pragma unroll
           for (int i = kKeys * h; i < kKeys * h + kKeys; i += 2) {
             float x0, x1;
-            fma2(x0, x1, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]), sl2, negm);
+            fma2(x0, x1, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]), ref.mul, ref.add);
             const float p0 = fast_exp2(x0);
             const float p1 = fast_exp2(x1);
             if ((i >> 1) & 1) add2(ls[2], ls[3], p0, p1); else add2(ls[0], ls[1], p0, p1);

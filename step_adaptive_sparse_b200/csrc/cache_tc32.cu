@@ -328,6 +328,7 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         mbar_arrive(bar(BAR_Q_FULL));
       }
       float m = -INFINITY, l = 0.f, o[D];
+      RowRef ref{sl2, 0.f};                // nothing seen so far: all weights 0
 #pragma unroll
       for (int i = 0; i < D; ++i) o[i] = 0.f;
       // adds tile k's output
@@ -376,17 +377,20 @@ cache_tc32_kernel(const __grid_constant__ UnitParams prm) {
         float pm[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
         for (int i = 4; i < kKT; i += 2) pm[(i >> 1) & 3] = max3(pm[(i >> 1) & 3], s[i], s[i + 1]);
-        const float mnew = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl2, m);
+        const float top = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+        const float mnew = fmaxf(top * sl2, m);
         const bool rescale = __any_sync(0xffffffffu, mnew > m + kRescaleThreshold);
         const float alpha = rescale ? (m == -INFINITY ? 0.f : fast_exp2(m - mnew)) : 1.f;
-        if (rescale) m = mnew;
+        if (rescale) {
+          if (mnew > m) ref = row_ref(top, mnew, sl2);
+          m = mnew;
+        }
         l *= alpha;
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
-        const float negm = m == -INFINITY ? 0.f : -m;     // nothing seen so far: all weights 0
 #pragma unroll
         for (int i = 0; i < kKT; i += 2) {
           float x0, x1;
-          fma2(x0, x1, s[i], s[i + 1], sl2, negm);
+          fma2(x0, x1, s[i], s[i + 1], ref.mul, ref.add);
           s[i] = fast_exp2(x0);
           s[i + 1] = fast_exp2(x1);
           if ((i >> 1) & 1) add2(ls[2], ls[3], s[i], s[i + 1]); else add2(ls[0], ls[1], s[i], s[i + 1]);

@@ -165,4 +165,27 @@ __host__ __device__ inline bool decode_unit(int idx, const UnitParams& p, Unit& 
   return true;
 }
 
+#ifdef __CUDACC__
+// A row's weights are 2^(s mul + add), one fused step: mul is the scale in base 2, add
+// minus the rounded product of it and the reference.  They share a factor 2^c,
+// |c| <= 2^-24 |add|, which the division cancels, but which leaves the number range
+// once the product passes 2^31.  A reference with a product m beyond kFar takes mul
+// down until it is kFar: |c| is then 2^6 at most, and scores that differ at all are
+// 2^6 apart still, so that those below the largest have no weight, as they should.
+// (Kept over the tiles: where the reference stays, nothing is computed.  Prompt of 8192
+// tokens, window 2048: 248 us, taking -m anew in every tile 250; four images 871, 887.)
+struct RowRef {
+  float mul, add;
+};
+constexpr float kFar = 1073741824.f;         // 2^30
+__device__ __forceinline__ RowRef row_ref(float top, float m, float sl2) {
+  RowRef r{sl2, -m};
+  if (fabsf(m) > kFar) {
+    r.mul = kFar / fabsf(top);
+    r.add = -(top * r.mul);
+  }
+  return r;
+}
+#endif
+
 }  // namespace area

@@ -802,3 +802,46 @@ def test_fp32_weights_keep_fp32(case):
     want, tol, got, wtol = cb.call(*x[:3], lens, cb.SCALE, lambda n: co.visible(n, Nq, S))
     close(o, want, tol)
     close(acco, got, wtol)
+
+
+# ---- infinities, and scores as large as they get ----------------------------------------------
+
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e9, 2e38])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S", [(1, 4, 2, 1, 500), (1, 64, 64, 300, 500), (2, 6, 2, 8, 5000)])
+def test_scores_of_any_size(B, H, Hk, Nq, S, dtype, size):
+    """One key of a score of +size, all others 0 or -size: the row is its value; without it, with
+    scores of 0 and -size, the mean of the values that have 0."""
+    D = 64
+    t = TYPES[dtype][0]
+    lens = [S] * B
+    dev, host, dl = make(123, dtype, B, H, Hk, Nq, S, D, lens)
+    q, k, v = dev[:3]
+    q.zero_(), k.zero_()
+    q[..., 7] = 1.0
+    big = float(torch.tensor(size, dtype=torch.bfloat16))
+    top = S - Nq // 2 - 1                       # seen by the later half of the rows
+    k[:, :, 1::3, 7] = -big
+    k[:, :, top] = 0
+    k[:, :, top, 7] = big
+    o = torch.full_like(q, NAN)
+    run_sink(dev, dl, dtype, INT_MAX, 0, 1.0, o)
+    pos = torch.arange(S - Nq, S, device="cuda")
+    sees = pos >= top
+    want = v[:, :, top].repeat_interleave(H // Hk, 1)[:, :, None].expand_as(o)
+    # one weight is all there is, but it need not be 1: the kernels for many rows take 2^(s a - M) in one
+    # step, M the rounded product of score and scale, which is 2^c with |c| <= 2^-24 M; bf16 rounds it to
+    # 8 bits for the product with the value, and divides by what it was: 2^-8; fp32 divides by the same
+    # value, with rounding errors of the product, the quotient and the result, under 2^-20
+    off = (2.0 ** -8 if dtype == "bf16" else 0) + 2.0 ** -20 + TYPES[dtype][2]
+    assert sees.any()
+    close(o[:, :, sees], want[:, :, sees].double().cpu().numpy(), off * want[:, :, sees].double().abs().cpu().numpy())
+    at = torch.arange(S, device="cuda")
+    zero = ((at % 3 != 1)[None, :] & (at[None, :] <= pos[:, None]) & (at != top)[None, :]).double()
+    mean = torch.einsum("ij,bhjd->bhid", zero / zero.sum(1, keepdim=True), v.double()).repeat_interleave(H // Hk, 1)
+    # exact weights of one: the sum's rounding and the result's, and bf16 weights of one are exact
+    size_ = torch.einsum("ij,bhjd->bhid", zero / zero.sum(1, keepdim=True), v.double().abs()).repeat_interleave(H // Hk, 1)
+    tol = (2.0 ** -20 + 8 * math.sqrt(S) * 2.0 ** -24) * size_ + TYPES[dtype][2] * mean.abs() + 1e-30
+    if (~sees).any():
+        close(o[:, :, ~sees], mean[:, :, ~sees].cpu().numpy(), tol[:, :, ~sees].cpu().numpy())
+    assert area.area_kernel_error() == 0
