@@ -473,7 +473,10 @@ int area_window_attn_noalloc(const void* q, const void* k, const void* v,
  *     p = lens[b] - Nq + i.  A query that sees no key (p < 0: a sequence
  *     shorter than Nq, padded in front) gets a row of zeros.
  *   - A non-finite key or value that some query of a sequence sees may reach
- *     every output row of the calls' sequences that read that key head.
+ *     every output row of the sequences that read that key head, as an infinity
+ *     or as a NaN: which of them hangs on the kernel that the sizes choose.  It
+ *     reaches no other key head and, in a cache, no other sequence.
+ *   - Scores, scale * q.k, are finite, also times log2(e).
  *   - ws   : workspace of ws_bytes >= area_*_ws_bytes() (host only, from the
  *     sizes alone; 0 = none, ws may then be null), 32-byte aligned.  Contents
  *     on entry are ignored, on exit unspecified; calls that may overlap on
@@ -514,7 +517,8 @@ int area_sink_attn(const void* q, const void* k, const void* v,
  *   causal = 0: prefix and own keys j < lens[b], for every query (several
  *               images of one prompt that share its text keys)
  * P = 0 (kp, vp null) or S = 0 (k, v null; lens is then not read) leave that
- * part out; one of them is positive.  When a sequence has few queries (fewer
+ * part out; one of them is positive.  (S = 0 goes with causal = 0: with 1 every
+ * query is before its sequence's first token and gets zeros.)  When a sequence has few queries (fewer
  * than 64 rows per key head) and the prefix is long, it is read once for the
  * batch, all sequences' rows against it, and joined with the own keys' part.
  */
@@ -534,7 +538,9 @@ int area_prefix_attn(const void* q, const void* kp, const void* vp,
  *   acco[b, hk, j] = acc[b, hk, j] + sum of the softmax weights of key j over
  *          the H / Hk query heads of hk and the Nq queries
  * acc, acco : fp32 [B, Hk, S]; acc null counts as zeros; acco may be acc.
- * Entries from lens[b] on are copied.
+ * Entries from lens[b] on are copied.  A weight is 2^(score - log-sum of its
+ * row) in fp32: next to the score's own rounding it is off by up to 2^-22 times
+ * the size of the row's largest score.
  */
 int area_cache_attn_ws_bytes(int B, int H, int Hk, int Nq, int S, int D,
                              int dtype, size_t* ws_bytes);

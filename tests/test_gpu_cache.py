@@ -806,6 +806,45 @@ def test_fp32_weights_keep_fp32(case):
 
 # ---- infinities, and scores as large as they get ----------------------------------------------
 
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), 3.3e38])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S", [(2, 4, 2, 1, 600), (2, 64, 64, 200, 600), (2, 8, 1, 3, 600)])
+def test_infinities_where_nobody_looks(B, H, Hk, Nq, S, dtype, bad):
+    """Behind the last token and between the sinks and the first window, in keys and in values."""
+    D, window, sinks, lens = 64, 70, 3, [S, 400]
+    dev, host, dl = make(121, dtype, B, H, Hk, Nq, S, D, lens)
+    want, got = (torch.full_like(dev[0], NAN) for _ in range(2))
+    run_sink(dev, dl, dtype, window, sinks, 0.125, want)
+    for x in dev[1:3]:
+        for b, n in enumerate(lens):
+            x[b, :, n:] = bad
+            x[b, :, sinks:n - Nq + 1 - window] = bad
+    run_sink(dev, dl, dtype, window, sinks, 0.125, got)
+    assert torch.equal(want, got) and torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), NAN])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,Nq,S", [(2, 4, 2, 1, 300), (2, 64, 32, 150, 300)])
+def test_what_is_seen_and_not_finite_stays_with_its_key_head(B, H, Hk, Nq, S, dtype, which, bad):
+    D, lens = 64, [S, S]
+    dev, host, dl = make(122, dtype, B, H, Hk, Nq, S, D, lens)
+    want, got = (torch.full_like(dev[0], NAN) for _ in range(2))
+    zero, acco = (torch.full((B, Hk, S), NAN, device="cuda") for _ in range(2))
+    run_cache(dev, dl, dtype, 0.125, None, want, zero)
+    dev[1 if which == "k" else 2][1, Hk - 1, S - Nq, 5] = bad         # the first query's own token
+    run_cache(dev, dl, dtype, 0.125, None, got, acco)
+    G = H // Hk
+    mine = torch.zeros(B, H, dtype=torch.bool)
+    mine[1, H - G:] = True
+    assert torch.equal(got[~mine], want[~mine])
+    assert torch.equal(acco.view(-1, S)[:-1], zero.view(-1, S)[:-1])
+    if which == "v":                            # it shows in its column for every row that gives it weight
+        assert not torch.isfinite(got[mine][:, 0, 5]).any()
+        assert torch.equal(acco, zero)
+
+
 @pytest.mark.parametrize("size", [1e3, 1e6, 1e9, 2e38])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("B,H,Hk,Nq,S", [(1, 4, 2, 1, 500), (1, 64, 64, 300, 500), (2, 6, 2, 8, 5000)])
