@@ -884,3 +884,123 @@ def test_scores_of_any_size(B, H, Hk, Nq, S, dtype, size):
     if (~sees).any():
         close(o[:, :, ~sees], mean[:, :, ~sees].cpu().numpy(), tol[:, :, ~sees].cpu().numpy())
     assert area.area_kernel_error() == 0
+
+
+# ---- many rows and evictions past 2^31 values, evictions in replayed graphs ----------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows_on_a_long_cache_past_32_bits(dtype):
+    """The kernels for many rows and their weights on more than 2^31 values per tensor: the last
+    head's rows lie past that.  All keys but the last 300 have a score 40 below theirs at least, so
+    that their part of a row is under S e^-32."""
+    B, H, Hk, Nq, S, D = 3, 2, 2, 200, 2_900_000, 128
+    t = TYPES[dtype][0]
+    n, tail, scale = S - 5, 300, 0.5
+    g = torch.Generator().manual_seed(131)
+    q = torch.randn(B, H, Nq, D, generator=g) * 0.2
+    kt, vt = torch.randn(B, Hk, tail, D, generator=g) * 0.2, torch.randn(B, Hk, tail, D, generator=g)
+    q[..., 0], kt[..., 0] = 10.0, 10.0                 # scores of 50, give or take 10 sd of 0.23
+    q, kt, vt = (x.to(t) for x in (q, kt, vt))
+    k = torch.zeros(B, Hk, S, D, dtype=t, device="cuda")
+    assert k.numel() > 2 ** 31
+    v = torch.zeros_like(k)
+    k[:, :, n - tail:n], v[:, :, n - tail:n] = kt.cuda(), vt.cuda()
+    lens = torch.full((B,), n, dtype=torch.int32).cuda()
+    host = [x.double().numpy() for x in (q, kt, vt)] + [np.zeros((Hk, 0, D))] * 2
+    dq, rest = q.cuda(), S * math.exp(-32)
+    o = torch.full((B, H, Nq, D), NAN, dtype=t, device="cuda")
+    run_sink((dq, k, v, None, None), lens, dtype, 128, 0, scale, o)
+    want, _, size = co.cache_attention(*host[:3], [tail] * B, scale, window=128)
+    # (q k is a sum of one large product and small ones: the docstring's bound takes all as large)
+    close(o, want, bound(host, want, size, dtype, scale, tail))
+    acco = torch.full((B, Hk, S), NAN, device="cuda")
+    run_cache((dq, k, v, None, None), lens, dtype, scale, None, o.fill_(NAN), acco)
+    want, got, size = co.cache_attention(*host[:3], [tail] * B, scale)
+    close(o, want, bound(host, want, size, dtype, scale, tail) + rest * (size + np.abs(want)))
+    have = acco[:, :, n - tail:n].double().cpu().numpy()
+    d = D * 2.0 ** -24 * scale * 11.0 * 11.0 * D       # as in test_cache_attention_and_weights
+    assert (np.abs(have - got) <= got * (4 * d + 2.0 ** -20 + (H // Hk * Nq + 2) * 2.0 ** -24) + rest * Nq).all()
+    assert (acco[:, :, n:] == 0).all() and acco[:, :, :n - tail].max() <= Nq * math.exp(-32)
+    assert area.area_kernel_error() == 0
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_eviction_past_32_bits(in_place):
+    B, Hk, S, D, budget, sinks, recent = 3, 2, 2_900_000, 128, 5000, 4, 1000
+    g = torch.Generator(device="cuda").manual_seed(141)
+    k = torch.empty(B, Hk, S, D, dtype=torch.bfloat16, device="cuda")
+    assert k.numel() > 2 ** 31
+    # a token's row says which it is, in four values of 7 bits and its head
+    at = torch.arange(S, device="cuda", dtype=torch.int32)
+    mark = torch.stack([at >> 21, at >> 14 & 127, at >> 7 & 127, at & 127], -1).bfloat16()
+    k.zero_()
+    for b in range(B):
+        for h in range(Hk):
+            k[b, h, :, D - 5:D - 1] = mark
+            k[b, h, :, D - 1] = 1 + b * Hk + h
+    v = -k
+    acc = torch.rand(B, Hk, S, generator=g, device="cuda")
+    lens = torch.tensor([S, S - 7, S - 100], dtype=torch.int32, device="cuda")
+    a0 = acc.clone()
+    So = S if in_place else budget
+    ko, vo, acco = (k, v, acc) if in_place else (torch.zeros(B, Hk, So, D, dtype=k.dtype, device="cuda"),
+                                                  torch.zeros(B, Hk, So, D, dtype=k.dtype, device="cuda"),
+                                                  torch.full((B, Hk, So), NAN, device="cuda"))
+    idx = torch.full((B, Hk, So), 7, dtype=torch.int32, device="cuda")
+    lenso = torch.zeros_like(lens)
+    area.area_cache_evict(k, v, acc, lens, ko, vo, acco, lenso, idx, B, Hk, S, So, D, budget, sinks, recent,
+                          area.AREA_DTYPE_BF16)
+    assert lenso.tolist() == [budget] * B
+    for b, n in enumerate([S, S - 7, S - 100]):
+        for h in range(Hk):
+            free = a0[b, h, sinks:n - recent]
+            best = torch.sort(free, descending=True, stable=True).indices[:budget - sinks - recent]
+            keep = torch.cat([at[:sinks].long(), best.sort().values + sinks, at[n - recent:n].long()])
+            assert torch.equal(idx[b, h, :budget].long(), keep) and (idx[b, h, budget:] == -1).all()
+            assert torch.equal(acco[b, h, :budget], a0[b, h, keep]) and (acco[b, h, budget:] == 0).all()
+            for x, sign in ((ko, 1), (vo, -1)):
+                rows = x[b, h, :budget].float() * sign
+                assert torch.equal(rows[:, D - 5:D - 1], mark[keep].float())
+                assert (rows[:, D - 1] == 1 + b * Hk + h).all() and (rows[:, :D - 5] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S", [700, 5000])
+def test_replayed_graphs_of_an_eviction_in_place(S, dtype):
+    """Captured with the copies that fill the cache: replays follow the lengths and the weights."""
+    B, Hk, D, budget, sinks, recent = 3, 4, 64, S // 2, 4, S // 8
+    t, dt, _ = TYPES[dtype]
+    g = torch.Generator(device="cuda").manual_seed(151)
+    k0, v0 = (torch.randn(B, Hk, S, D, generator=g, device="cuda").to(t) for _ in range(2))
+    acc0 = torch.rand(B, Hk, S, generator=g, device="cuda")
+    k, v, acc = k0.clone(), v0.clone(), acc0.clone()
+    lens = torch.tensor([S, S - 1, 3], dtype=torch.int32, device="cuda")
+    lenso, idx = torch.zeros_like(lens), torch.zeros(B, Hk, S, dtype=torch.int32, device="cuda")
+
+    def step(s):
+        k.copy_(k0), v.copy_(v0), acc.copy_(acc0)
+        area.area_cache_evict(k, v, acc, lens, k, v, acc, lenso, idx, B, Hk, S, S, D, budget, sinks, recent, dt, s)
+
+    step(None)
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        step(torch.cuda.current_stream())
+    for new in ([S, S - 1, 3], [budget, budget + 1, 0], [S // 3, S, S]):
+        lens.copy_(torch.tensor(new, dtype=torch.int32))
+        acc0.copy_(torch.rand(B, Hk, S, generator=g, device="cuda"))
+        step(None)
+        torch.cuda.synchronize()
+        want = [x.clone() for x in (k, v, acc, lenso, idx)]
+        for x in (k, v, acc, lenso, idx):
+            x.fill_(5)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((k, v, acc, lenso, idx), want))
+        for b in range(B):
+            keep = co.kept_tokens(acc0[b, 1].tolist(), new[b], budget, sinks, recent)
+            assert idx[b, 1, :len(keep)].tolist() == keep
+            assert torch.equal(k[b, 1, :len(keep)], k0[b, 1, keep])
