@@ -9,6 +9,9 @@ namespace {
 
 constexpr int64_t kSms = 148;        // B200; the workspace's size may not hang on the device
 
+// Most keys of a unit of the kernels for many rows: a role may wait for another through
+// a whole unit, 0.4 s with as many (fp32, D = 128), and waits end after 2 s.
+constexpr int64_t kUnitKeys = 1 << 23;
 constexpr double kPoolBytes = 32 << 20;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -128,6 +131,7 @@ void cut(CacheLaunch& l, int op, int dtype, int64_t few_keys, int64_t many_keys,
     // 5.6 us (fp32, 128 rows, D = 64 or 128)
     const double tile = dtype == AREA_DTYPE_BF16 ? 2.1 : D == 64 ? 3.2 : 5.6;
     n = best_split({blocks, keys, kSms, rows, D, 4.0, tile / 128, 1.0}, cdiv(keys, 256));
+    n = std::max(n, cdiv(keys, kUnitKeys));
   } else {
     const int64_t slots = few_per_sm(dtype, D) * kSms;
     if (blocks * 8 <= slots && (keys <= 4096 || blocks * 8 >= 2 * kSms)) {
@@ -219,8 +223,10 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   p->off_logits = p->off_lse + (weights && !few ? ceil256(p->rows * 4) : 0);
   if (p->rows > (int64_t(1) << 58) / (S + 1)) return AREA_EUNSUPPORTED;
   p->bytes = p->off_logits + (weights && few ? ceil256(p->rows * S * 4) : 0);
-  const int64_t blocks = cdiv(m.rows.RG, 8) * m.rows.groups * std::max(m.nsplit, 1);
-  if (blocks > INT_MAX || cdiv(S, 128) * B * Hk > INT_MAX ||
+  auto blocks = [&](const CacheLaunch& l) {
+    return l.used ? cdiv(l.rows.RG, rows_per_block(l.kernel, dtype, l.rows)) * l.rows.groups * l.nsplit : 0;
+  };
+  if (blocks(m) > INT_MAX - 1024 || blocks(p->pooled) > INT_MAX - 1024 || cdiv(S, 128) * B * Hk > INT_MAX ||
       (weights && few && p->rows + cdiv(S, 512) * B * Hk > INT_MAX))
     return AREA_EUNSUPPORTED;
   return AREA_OK;

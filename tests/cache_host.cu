@@ -18,6 +18,18 @@ int host_pools(int B, int H, int Hk, int Nq, int P, int S, int D, int dtype) {
   if (area::cache_plan(area::CACHE_OP_PREFIX, B, H, Hk, Nq, P, S, D, INT_MAX, 0, dtype, &p) != AREA_OK) return -1;
   return p.pooled.used;
 }
+// Most keys of a unit of the kernels for many rows (0: the call has none); -1: refused.
+int64_t host_unit_keys(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int dtype) {
+  area::CachePlan p;
+  if (area::cache_plan(op, B, H, Hk, Nq, P, S, D, INT_MAX, 0, dtype, &p) != AREA_OK) return -1;
+  int64_t most = 0;
+  for (const area::CacheLaunch* l : {&p.main, &p.pooled})
+    if (l->used && l->kernel == area::CACHE_TC) {
+      const int64_t keys = (l->rows.use_prefix ? (int64_t)P : 0) + (l->rows.use_own ? S : 0);
+      most = std::max(most, (keys + l->nsplit - 1) / l->nsplit);
+    }
+  return most;
+}
 int host_share_of(int n, int part, int parts) { return area::share_of(n, part, parts); }
 }
 
