@@ -518,9 +518,10 @@ int area_sink_attn(const void* q, const void* k, const void* v,
  *               images of one prompt that share its text keys)
  * P = 0 (kp, vp null) or S = 0 (k, v null; lens is then not read) leave that
  * part out; one of them is positive.  (S = 0 goes with causal = 0: with 1 every
- * query is before its sequence's first token and gets zeros.)  When a sequence has few queries (fewer
- * than 64 rows per key head) and the prefix is long, it is read once for the
- * batch, all sequences' rows against it, and joined with the own keys' part.
+ * query is before its sequence's first token and gets zeros.)  When a sequence
+ * has few queries (fewer than 64 rows per key head) and the prefix is long, it
+ * is read once for the batch, all sequences' rows against it, and joined with
+ * the own keys' part.
  */
 int area_prefix_attn_ws_bytes(int B, int H, int Hk, int Nq, int P, int S,
                               int D, int dtype, size_t* ws_bytes);

@@ -190,7 +190,14 @@ int cache_plan(int op, int B, int H, int Hk, int Nq, int P, int S, int D, int wi
   const int R = H / Hk * Nq;
   // Few rows of a sequence: the prefix against the rows of all sequences, once
   // it is so large that reading it from L2 for each costs more than the second
-  // launch and the join.
+  // launch and the join.  Pooled / not, us, by the bytes that all sequences would read,
+  // bf16: 6 MB 15.1 / 11.5; 31 MB 15.5 / 16.6 and 15.1 / 13.8; 62 MB 22.6 / 19.0 and
+  // 22.9 / 27.4; 125 MB 23.4 / 39.6 and 26.0 / 26.5; 938 MB 43 / 188.  fp32: 31 MB 23 /
+  // 18, 62 MB 25 / 17 to 33 / 42, 250 MB 39 / 47, 938 MB and more 95 / 533.  (30000
+  // keys, 64 sequences, bf16, by the rows: 32: 56 / 190; 48: 78 / 192.  Of 64 rows on
+  // two sequences fill a row tile, or one: 64: 80 / 194, 128: 140 / 201, but with 8
+  // sequences 40 / 38 and 43 / 40, with two 28 / 27 and 38 / 29; fp32 335 / 615 and
+  // 666 / 658.  The limit is on the safe side for small batches; large ones would gain.)
   const double pre = (double)B * Hk * P * D * (dtype == AREA_DTYPE_BF16 ? 4 : 8);
   const bool pool = op == CACHE_OP_PREFIX && P > 0 && B > 1 && R < 64 && pre > kPoolBytes;
   p->pooled = CacheLaunch{};

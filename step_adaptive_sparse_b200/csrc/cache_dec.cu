@@ -15,8 +15,11 @@
 // 16 keys and values (8 KB at D = 128) in flight.
 // The softmax keeps one reference per row and rescales only when a score
 // exceeds it by more than 2^8 (numerator and denominator use the same one, so
-// the result is exact); the weights are rounded once, to bf16, for the second
-// product.  mma.sync is enough here: at 8 rows the products take a fifth of
+// the result is exact).  The weights are rounded once, to bf16: an mma takes both its
+// factors in one type, and the values have that one.  It costs a row 2^-8 of its
+// weighted values at most (measured: outputs off by 2.3e-3 rms of their size on long
+// caches, 1.7e-3 with weights of 32 bits, which is the output's own rounding).
+// mma.sync is enough here: at 8 rows the products take a fifth of
 // the time that the keys take to arrive.
 #include "cache_dec.cuh"
 

@@ -3,7 +3,8 @@
 // Of a sequence of n > budget tokens each key head keeps the first `sinks`,
 // the last `recent` and, of the tokens between, the budget - sinks - recent
 // with the largest accumulated weight (ties: the lowest index), in their
-// order.  One launch chooses and copies; in place the rows move in a second.
+// order.  One launch chooses, and copies where the cache is short; in long caches a second
+// one copies, in place a second one moves the rows.
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
@@ -284,7 +285,10 @@ __global__ void __launch_bounds__(kThreads) evict_copy_kernel(const EvictArgs e,
 // The copy within the cache itself.  A kept row moves to an index not above
 // its own, so a block that moves rows in ascending order, all of a step read
 // before any is written, never writes a row that is still to be read.  A block
-// has one 64-byte column of K or V, or the weights, of a key head.
+// has one 64-byte column of K or V, or the weights, of a key head.  The steps of a block
+// follow one another, which bounds the call where heads are few: 8 heads of 40000
+// tokens to 20000 take 245 us in bf16 (copied: 47) and 265 in fp32 (72); 256 heads of
+// 8192 to 4096 in bf16 220 (186), 128 in fp32 213 (180).
 constexpr int kMoveRows = 4;                             // rows of a thread and step
 __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs e, int cols) {
   wait_for_last();
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs e, int 
 
 // Blocks of a cluster: a share of `least` candidates at least, and four blocks to an
 // SM at most (256 heads of 8192 tokens: 2 blocks 183 us, 8 blocks 217; 8 heads of
-// 40000: 8 blocks 31 us, 2 blocks 56; 2048 heads of 500: one block 73, 2 blocks 100).
+// 40000 to 10000: 8 blocks 31 us, 2 blocks 56; 2048 heads of 500: one block 73, 2 blocks 100).
 int evict_cluster(int heads, int S, int least, int most) {
   int cs = 1;
   while (cs < most && S > least * cs && (int64_t)heads * cs * 2 <= 4 * 148) cs *= 2;
@@ -347,7 +351,7 @@ int evict_cluster(int heads, int S, int least, int most) {
 cudaError_t launch_cache_evict(const EvictArgs& e, cudaStream_t s) {
   // Short caches: the blocks that choose also copy (2 heads of 600 tokens: 9.1 us, with
   // a launch for the copy 11.6; 2048 heads of 500: 73 and 80).  Long ones: more blocks
-  // copy than choose (8 heads of 40000: 31 us, in one launch 51; 256 of 8192: 183, 196).
+  // copy than choose (8 heads of 40000 to 10000: 31 us, in one launch 51; 256 of 8192: 183, 196).
   const int heads = e.B * e.Hk;
   const bool in_place = e.k == e.ko, one = !in_place && e.S <= kTile;
   const int cs = one ? evict_cluster(heads, e.S, 256, 4) : evict_cluster(heads, e.S, 1024, 8);
